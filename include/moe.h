@@ -85,6 +85,18 @@ typedef struct {
                        the MoE Serving Tax, "Padding model (Section 5.1)") */
 } moe_config_t;
 
+/* The norms around a block (moe_block_norm and its relatives). */
+typedef struct {
+    int T;            /* tokens, >= 0 */
+    int H;            /* hidden size: 16-byte rows, at most 32 KB per row
+                         (H <= 16384 in bf16, 8192 in fp32) */
+    int dtype;        /* 0 = bf16, 1 = fp32 */
+    int gate_mode;    /* 0: no gate; 1: one gate per channel [H];
+                         2: one per token and channel [T, H] */
+    float eps;        /* added to the mean square, > 0 */
+    float res_scale;  /* scale of the residual */
+} moe_norm_config_t;
+
 /* Text for a status code (static storage). */
 const char* moe_status_string(int status);
 
@@ -473,6 +485,123 @@ int moe_tp_gather(int n_chunks, const float* const* parts, int T, int H, int dty
  * GPUs: an event or a barrier) and keeps the parts alive until it ends. */
 int moe_tp_reduce(int n_parts, const float* const* parts, long long count, int dtype, void* out,
                   moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Training.  The gradients of the layer's steps, each from the tensors its
+ * forward step read or wrote; the norms around the block; and the gradients
+ * of the experts' products.  A training step of the MoE block is
+ *   forward:  moe_router_gemm, moe_route, moe_align_pad, moe_permute,
+ *             moe_grouped_gate_up_train, moe_grouped_down, moe_combine_norm;
+ *   backward: moe_block_norm_grad, moe_combine_grad, moe_grouped_down_grad,
+ *             moe_grouped_down_wgrad, moe_grouped_gate_up_grad,
+ *             moe_grouped_gate_up_wgrad, moe_permute_grad, moe_route_grad.
+ * The pages cover the forward only; these follow from its formulas.  Sums are
+ * fp32 in a fixed order (results are the same from run to run) and every
+ * output is rounded once.  Rows of permuted buffers at and past P are left
+ * untouched. */
+
+/* Gradient of the combine: with dout [T, H] the gradient of its output,
+ *   dy_perm[pos(t,k)] = topk_w[t,k] * dout[t]      (padding rows p < P: zero)
+ *   dtopk_w[t,k]      = <dout[t], y_perm[pos(t,k)]>   (0 for an empty slot).
+ * The gradient of the shared output is dout itself.  y_perm, pos and topk_w
+ * as the combine read them, sorted_ids and scalars from the alignment.
+ * dy_perm [P_max, H] may be y_perm itself.  H * element size at most 32 KB. */
+int moe_combine_grad(const moe_config_t* cfg, const void* dout, const void* y_perm, const int32_t* pos,
+                     const float* topk_w, const int32_t* sorted_ids, const int32_t* scalars, void* dy_perm,
+                     float* dtopk_w, moe_stream_t stream);
+
+/* Gradient of the permute: dx[t] = sum_k dx_perm[pos(t,k)] (+ dx_add[t]),
+ * fp32 in ascending k, dx_add (nullable [T, H]: the gradient that reaches x
+ * another way, e.g. through the shared experts or the router) added last. */
+int moe_permute_grad(const moe_config_t* cfg, const void* dx_perm, const int32_t* pos, const void* dx_add,
+                     void* dx, moe_stream_t stream);
+
+/* Gradient of the top-K gate: dlogits [T, E] (fp32, every entry written) from
+ * dtopk_w [T, K], the logits and the selected ids, for cfg->score_fn and
+ * renorm.  With w the gate weights, p the softmax over E, s the sigmoid:
+ *   softmax, renorm: w_i (dw_i - sum_j w_j dw_j) on the selected, else 0;
+ *   softmax:         p_e (dw_e [e selected] - sum_j p_j dw_j) on every e;
+ *   sigmoid, renorm: w_i (1 - s_i) (dw_i - sum_j w_j dw_j) on the selected;
+ *   sigmoid:         s_i (1 - s_i) dw_i on the selected.
+ * Empty slots (id -1, per-token dynamic K) and ids outside [0, E) carry no
+ * gradient; their dtopk_w is not read. */
+int moe_route_grad(const moe_config_t* cfg, const float* logits, const int32_t* topk_ids, const float* dtopk_w,
+                   float* dlogits, moe_stream_t stream);
+
+/* The norms after a block and before the next, with the block's gate and the
+ * residual's scale, in one launch.  For every token, in fp32,
+ *   z = y * rsqrt(mean(y^2) + eps) * w_post     (z = y when w_post is NULL)
+ *   h = res_scale * residual + gate * z         (residual, gate: where given)
+ *   n = h * rsqrt(mean(h^2) + eps) * w_next     (when w_next is given)
+ * y, residual, h, n [T, H]; w_post, w_next [H]; gate by gate_mode; all in
+ * the activation dtype.  y NULL: only the norm before a block (h =
+ * res_scale * residual; no w_post or gate then).  residual NULL: none.  n is
+ * given with w_next and only then; h may be NULL beside n.  n is computed
+ * from h before its rounding.  h may be residual or y itself (in place). */
+int moe_block_norm(const moe_norm_config_t* nc, const void* y, const void* residual, const void* w_post,
+                   const void* gate, const void* w_next, void* h, void* n, moe_stream_t stream);
+
+/* moe_combine and moe_block_norm in one launch: y is the combine's sum
+ * (y_perm, pos, topk_w, shared_out as for moe_combine), used before its
+ * rounding; y_out (nullable [T, H]) receives it rounded, for the gradient.
+ * nc's T, H and dtype are cfg's.  One token costs one launch and K + 1 rows. */
+int moe_combine_norm(const moe_config_t* cfg, const moe_norm_config_t* nc, const void* y_perm, const int32_t* pos,
+                     const float* topk_w, const void* shared_out, const void* residual, const void* w_post,
+                     const void* gate, const void* w_next, void* y_out, void* h, void* n, moe_stream_t stream);
+
+/* Bytes of workspace moe_block_norm_grad needs on the current device (0 on a
+ * bad configuration).  It need not be zeroed. */
+size_t moe_block_norm_grad_workspace_size(const moe_norm_config_t* nc);
+
+/* Gradient of moe_block_norm (and of the norm part of moe_combine_norm, with
+ * y its y_out): from dh [T, H] and dn [T, H], the gradients that reach h and n
+ * (either may be NULL; dn is given with w_next and only then, and needs h),
+ *   d         = dh + (gradient of n in h)
+ *   dresidual = res_scale * d                        [T, H], nullable
+ *   dgate     = d * z   ([H] fp32, summed over the tokens, in gate_mode 1;
+ *               [T, H] in gate_mode 2; given with gate and only then)
+ *   dy        = gradient of gate * z in y, times d   [T, H], given with y
+ *   dw_post, dw_next [H] fp32, summed over the tokens; nullable.
+ * h as the forward stored it (residual itself where res_scale is 1 and the
+ * forward had no y).  dresidual may be dh itself, dy may be dn or y.  T = 0
+ * writes zero dw_post, dw_next and gate_mode 1 dgate. */
+int moe_block_norm_grad(const moe_norm_config_t* nc, const void* h, const void* dh, const void* dn, const void* y,
+                        const void* w_post, const void* gate, const void* w_next, void* dresidual, void* dy,
+                        void* dgate, float* dw_post, float* dw_next, void* workspace, size_t ws_bytes,
+                        moe_stream_t stream);
+
+/* The experts' products of a training step, bf16 only (cfg->dtype 0), tile_B
+ * a multiple of 16 (MOE_ERR_ARG otherwise): segments are then whole tensor-core
+ * steps of 16 rows.  Workspace and its status as for moe_grouped_ffn
+ * (moe_gemm_workspace_size(), moe_check_status).  Padding rows of the row
+ * buffers must be zero, as moe_permute, moe_combine_grad and these calls
+ * leave them.
+ *
+ * moe_grouped_gate_up with the pre-activations kept: h13[p] = x_perm[p] .
+ * W13_e^T ([P_max, 2I], gate then up columns) and act[p] = silu(gate) * up
+ * ([P_max, I]), both rounded once from the fp32 sums. */
+int moe_grouped_gate_up_train(const moe_config_t* cfg, const void* x_perm, const void* w13, const int32_t* offsets,
+                              void* h13, void* act, void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/* Gradient through the down projection and SwiGLU: with dact[p] = dy_perm[p] .
+ * W2_e (never stored) and (g, u) = h13[p],
+ *   dh13[p] = (dact u silu'(g), dact silu(g))   ([P_max, 2I]; may be h13 itself),
+ *   silu'(g) = s (1 + g (1 - s)), s = 1 / (1 + exp(-g)). */
+int moe_grouped_down_grad(const moe_config_t* cfg, const void* dy_perm, const void* w2, const void* h13,
+                          const int32_t* offsets, void* dh13, void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/* Gradient through the gate/up projections: dx_perm[p] = dh13[p] . W13_e. */
+int moe_grouped_gate_up_grad(const moe_config_t* cfg, const void* dh13, const void* w13, const int32_t* offsets,
+                             void* dx_perm, void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/* Weight gradients, every expert's written (zeros for one without tokens):
+ *   dw2[e]  [H, I]  = sum over e's rows of dy_perm[p] (outer) act[p]
+ *   dw13[e] [2I, H] = sum over e's rows of dh13[p] (outer) x_perm[p]
+ * in bf16, summed in fp32.  T = 0 writes zeros. */
+int moe_grouped_down_wgrad(const moe_config_t* cfg, const void* dy_perm, const void* act, const int32_t* offsets,
+                           void* dw2, void* workspace, size_t ws_bytes, moe_stream_t stream);
+int moe_grouped_gate_up_wgrad(const moe_config_t* cfg, const void* dh13, const void* x_perm, const int32_t* offsets,
+                              void* dw13, void* workspace, size_t ws_bytes, moe_stream_t stream);
 
 /* Test hook: when nonzero, the next GEMM or fused-FFN launch withholds one
  * operand load (the first load of block 0, or of work item 0 in the fused

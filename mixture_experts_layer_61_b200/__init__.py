@@ -41,6 +41,16 @@ class MoeConfig(ctypes.Structure):
 
 
 BLOCKWISE, MAXVALUE = 0, 1  # padding schemes of the alignment
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN = 0, 1, 2  # gate of the block norms: none, [H], [T, H]
+
+
+class NormConfig(ctypes.Structure):
+    """moe_norm_config_t (include/moe.h)."""
+    _fields_ = [(n, ctypes.c_int) for n in ("T", "H", "dtype", "gate_mode")] + \
+               [(n, ctypes.c_float) for n in ("eps", "res_scale")]
+
+    def __repr__(self):
+        return "NormConfig(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
 
 
 def config(T, H, E, K, I, n_shared=0, I_shared=0, tile_B=16, score_fn=SOFTMAX, renorm=1, dtype=BF16,
@@ -48,6 +58,12 @@ def config(T, H, E, K, I, n_shared=0, I_shared=0, tile_B=16, score_fn=SOFTMAX, r
     if isinstance(dtype, torch.dtype):
         dtype = BF16 if dtype == torch.bfloat16 else FP32
     return MoeConfig(T, H, E, K, I, n_shared, I_shared, tile_B, score_fn, renorm, dtype, pad_mode)
+
+
+def norm_config(T, H, eps=1e-6, res_scale=1.0, gate_mode=GATE_NONE, dtype=BF16):
+    if isinstance(dtype, torch.dtype):
+        dtype = BF16 if dtype == torch.bfloat16 else FP32
+    return NormConfig(T, H, dtype, gate_mode, eps, res_scale)
 
 
 def lib():
@@ -60,6 +76,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
         C = ctypes.POINTER(MoeConfig)
+        N = ctypes.POINTER(NormConfig)
         sig = {
             "moe_status_string": (ctypes.c_char_p, [I]),
             "moe_padded_rows_max": (ctypes.c_int64, [C]),
@@ -101,6 +118,18 @@ def lib():
             "moe_tp_reduce": (I, [I, ctypes.POINTER(ctypes.c_void_p), ctypes.c_longlong, I, P, P]),
             "moe_layer_forward_partial_front": (I, [C, P, P, P, P, P, P, P, P, S, P, P]),
             "moe_layer_forward_partial_down": (I, [C, P, I, I, P, P, S, P]),
+            "moe_combine_grad": (I, [C, P, P, P, P, P, P, P, P, P]),
+            "moe_permute_grad": (I, [C, P, P, P, P, P]),
+            "moe_route_grad": (I, [C, P, P, P, P, P]),
+            "moe_block_norm": (I, [N, P, P, P, P, P, P, P, P]),
+            "moe_combine_norm": (I, [C, N, P, P, P, P, P, P, P, P, P, P, P, P]),
+            "moe_block_norm_grad_workspace_size": (S, [N]),
+            "moe_block_norm_grad": (I, [N, P, P, P, P, P, P, P, P, P, P, P, P, P, S, P]),
+            "moe_grouped_gate_up_train": (I, [C, P, P, P, P, P, P, S, P]),
+            "moe_grouped_down_grad": (I, [C, P, P, P, P, P, P, S, P]),
+            "moe_grouped_gate_up_grad": (I, [C, P, P, P, P, P, S, P]),
+            "moe_grouped_down_wgrad": (I, [C, P, P, P, P, P, S, P]),
+            "moe_grouped_gate_up_wgrad": (I, [C, P, P, P, P, P, S, P]),
             "moe_tp_gather": (I, [I, ctypes.POINTER(ctypes.c_void_p), I, I, I, P, P]),
         }
         for name, (res, args) in sig.items():
@@ -136,6 +165,18 @@ def _need_cuda(*ts):
     for t in ts:
         if t is not None and (not t.is_cuda or not t.is_contiguous()):
             raise ValueError("tensors must be contiguous CUDA tensors")
+
+
+def _arg(name, t, shape, dtype):
+    """One tensor argument of the training operators: on the current device,
+    contiguous, of this type and shape (None passes)."""
+    if t is None:
+        return
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current CUDA device")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                         f"not {t.dtype} {tuple(t.shape)}")
 
 
 def _act_dtype(cfg):
@@ -588,3 +629,221 @@ def tp_layer_forward(cfg_local, x, w_r, w13, w2, ws, w13_sh=None, w2_sh=None, lo
                                     k=k)
     tp_allreduce(partial, group)
     return tp_reduce([partial], out, dtype=x.dtype)
+
+
+# --------------------------------------------------------------- training
+# The gradients of the layer's steps and the norms around the block.  Buffers
+# with P_max rows are padded_rows_max(cfg) long; their rows at and past P are
+# left untouched.
+
+def _perm_arg(cfg, name, t, width, dtype=None):
+    _arg(name, t, (max(padded_rows_max(cfg), 1), width), dtype or _act_dtype(cfg))
+
+
+def combine_grad(cfg, dout, y_perm, pos, w, sorted_ids, scalars, dy_perm=None, dw=None):
+    """(dy_perm, dw) of the combine; dy_perm may be y_perm itself."""
+    dt = _act_dtype(cfg)
+    _arg("dout", dout, (cfg.T, cfg.H), dt)
+    _perm_arg(cfg, "y_perm", y_perm, cfg.H)
+    _arg("pos", pos, (cfg.T * cfg.K,), torch.int32)
+    _arg("w", w, (cfg.T, cfg.K), torch.float32)
+    _arg("sorted_ids", sorted_ids, (padded_rows_max(cfg),), torch.int32)
+    _arg("scalars", scalars, (4,), torch.int32)
+    if dy_perm is None:
+        dy_perm = torch.empty_like(y_perm)
+    if dw is None:
+        dw = torch.empty((cfg.T, cfg.K), dtype=torch.float32, device=dout.device)
+    _perm_arg(cfg, "dy_perm", dy_perm, cfg.H)
+    _arg("dw", dw, (cfg.T, cfg.K), torch.float32)
+    _check(lib().moe_combine_grad(ctypes.byref(cfg), _p(dout), _p(y_perm), _p(pos), _p(w), _p(sorted_ids),
+                                  _p(scalars), _p(dy_perm), _p(dw), _stream()), "moe_combine_grad")
+    return dy_perm, dw
+
+
+def permute_grad(cfg, dx_perm, pos, dx_add=None, dx=None):
+    """dx [T, H] of the permute, plus dx_add."""
+    dt = _act_dtype(cfg)
+    _perm_arg(cfg, "dx_perm", dx_perm, cfg.H)
+    _arg("pos", pos, (cfg.T * cfg.K,), torch.int32)
+    _arg("dx_add", dx_add, (cfg.T, cfg.H), dt)
+    if dx is None:
+        dx = torch.empty((cfg.T, cfg.H), dtype=dt, device=dx_perm.device)
+    _arg("dx", dx, (cfg.T, cfg.H), dt)
+    _check(lib().moe_permute_grad(ctypes.byref(cfg), _p(dx_perm), _p(pos), _p(dx_add), _p(dx), _stream()),
+           "moe_permute_grad")
+    return dx
+
+
+def route_grad(cfg, logits, ids, dw, dlogits=None):
+    """dlogits [T, E] of the top-K gate from the gate weights' gradient."""
+    _arg("logits", logits, (cfg.T, cfg.E), torch.float32)
+    _arg("ids", ids, (cfg.T, cfg.K), torch.int32)
+    _arg("dw", dw, (cfg.T, cfg.K), torch.float32)
+    if dlogits is None:
+        dlogits = torch.empty((cfg.T, cfg.E), dtype=torch.float32, device=logits.device)
+    _arg("dlogits", dlogits, (cfg.T, cfg.E), torch.float32)
+    _check(lib().moe_route_grad(ctypes.byref(cfg), _p(logits), _p(ids), _p(dw), _p(dlogits), _stream()),
+           "moe_route_grad")
+    return dlogits
+
+
+def _norm_args(nc, residual, w_post, gate, w_next, h, n):
+    dt, TH = _act_dtype(nc), (nc.T, nc.H)
+    _arg("residual", residual, TH, dt)
+    _arg("w_post", w_post, (nc.H,), dt)
+    _arg("w_next", w_next, (nc.H,), dt)
+    _arg("gate", gate, TH if nc.gate_mode == GATE_TOKEN else (nc.H,), dt)
+    _arg("h", h, TH, dt)
+    _arg("n", n, TH, dt)
+
+
+def block_norm(nc, residual=None, y=None, w_post=None, gate=None, w_next=None, h=None, n=None):
+    """(h, n): h = res_scale * residual + gate * norm(y, w_post), n =
+    norm(h, w_next) (None without w_next).  Without y only the norm before a
+    block: h is then written only when given."""
+    ref = y if y is not None else residual
+    if ref is None:
+        raise ValueError("block_norm needs y or residual")
+    _arg("y", y, (nc.T, nc.H), _act_dtype(nc))
+    if h is None and (y is not None or w_next is None):
+        h = torch.empty_like(ref)
+    if n is None and w_next is not None:
+        n = torch.empty_like(ref)
+    _norm_args(nc, residual, w_post, gate, w_next, h, n)
+    _check(lib().moe_block_norm(ctypes.byref(nc), _p(y), _p(residual), _p(w_post), _p(gate), _p(w_next), _p(h), _p(n),
+                                _stream()), "moe_block_norm")
+    return h, n
+
+
+def combine_norm(cfg, nc, y_perm, pos, w, shared_out=None, residual=None, w_post=None, gate=None, w_next=None,
+                 h=None, n=None, y=None, save_y=False):
+    """(h, n, y): combine and block_norm in one launch; y is the combine's
+    output, kept when a buffer is given or save_y is set (None otherwise)."""
+    dt, TH = _act_dtype(cfg), (cfg.T, cfg.H)
+    _perm_arg(cfg, "y_perm", y_perm, cfg.H)
+    _arg("pos", pos, (cfg.T * cfg.K,), torch.int32)
+    _arg("w", w, (cfg.T, cfg.K), torch.float32)
+    _arg("shared_out", shared_out, TH, dt)
+    if h is None:
+        h = torch.empty(TH, dtype=dt, device=y_perm.device)
+    if n is None and w_next is not None:
+        n = torch.empty(TH, dtype=dt, device=y_perm.device)
+    if y is None and save_y:
+        y = torch.empty(TH, dtype=dt, device=y_perm.device)
+    _arg("y", y, TH, dt)
+    _norm_args(nc, residual, w_post, gate, w_next, h, n)
+    _check(lib().moe_combine_norm(ctypes.byref(cfg), ctypes.byref(nc), _p(y_perm), _p(pos), _p(w), _p(shared_out),
+                                  _p(residual), _p(w_post), _p(gate), _p(w_next), _p(y), _p(h), _p(n), _stream()),
+           "moe_combine_norm")
+    return h, n, y
+
+
+def block_norm_grad_workspace_size(nc):
+    n = lib().moe_block_norm_grad_workspace_size(ctypes.byref(nc))
+    if n == 0:
+        raise MoeError(-1, "moe_block_norm_grad_workspace_size")
+    return n
+
+
+def block_norm_grad(nc, ws, h=None, dh=None, dn=None, y=None, w_post=None, gate=None, w_next=None, dresidual=None,
+                    dy=None, residual=True):
+    """The gradients of block_norm / combine_norm as a dict: dw_next,
+    dresidual, dgate, dw_post, dy (None where the form has none; residual
+    False leaves dresidual out)."""
+    dt, TH = _act_dtype(nc), (nc.T, nc.H)
+    dev = ws.device
+    _arg("ws", ws, (ws.numel(),), torch.uint8)
+    for name, t in (("dh", dh), ("dn", dn), ("y", y)):
+        _arg(name, t, TH, dt)
+    _norm_args(nc, None, w_post, gate, w_next, h, None)
+
+    def new(cond, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=dev) if cond else None
+
+    if dresidual is None:
+        dresidual = new(residual, TH, dt)
+    if dy is None:
+        dy = new(y is not None, TH, dt)
+    _arg("dresidual", dresidual, TH, dt)
+    _arg("dy", dy, TH, dt)
+    dgate = None
+    if gate is not None:
+        dgate = new(True, TH, dt) if nc.gate_mode == GATE_TOKEN else new(True, (nc.H,), torch.float32)
+    dw_post = new(w_post is not None, (nc.H,), torch.float32)
+    dw_next = new(w_next is not None, (nc.H,), torch.float32)
+    _check(lib().moe_block_norm_grad(ctypes.byref(nc), _p(h), _p(dh), _p(dn), _p(y), _p(w_post), _p(gate),
+                                     _p(w_next), _p(dresidual), _p(dy), _p(dgate), _p(dw_post), _p(dw_next), _p(ws),
+                                     ws.numel(), _stream()), "moe_block_norm_grad")
+    return dict(dw_next=dw_next, dresidual=dresidual, dgate=dgate, dw_post=dw_post, dy=dy)
+
+
+def _product_args(cfg, offsets, ws, w13=None, w2=None):
+    _arg("offsets", offsets, (cfg.E + 1,), torch.int32)
+    _arg("ws", ws, (ws.numel(),), torch.uint8)
+    _arg("w13", w13, (cfg.E, 2 * cfg.I, cfg.H), _act_dtype(cfg))
+    _arg("w2", w2, (cfg.E, cfg.H, cfg.I), _act_dtype(cfg))
+
+
+def _rows_like(cfg, t, width, out):
+    return torch.empty((max(padded_rows_max(cfg), 1), width), dtype=t.dtype, device=t.device) if out is None else out
+
+
+def grouped_gate_up_train(cfg, x_perm, w13, offsets, ws, h13=None, act=None):
+    """(h13, act): gate/up with the pre-activations [P_max, 2I] kept."""
+    _product_args(cfg, offsets, ws, w13=w13)
+    _perm_arg(cfg, "x_perm", x_perm, cfg.H)
+    h13, act = _rows_like(cfg, x_perm, 2 * cfg.I, h13), _rows_like(cfg, x_perm, cfg.I, act)
+    _perm_arg(cfg, "h13", h13, 2 * cfg.I)
+    _perm_arg(cfg, "act", act, cfg.I)
+    _check(lib().moe_grouped_gate_up_train(ctypes.byref(cfg), _p(x_perm), _p(w13), _p(offsets), _p(h13), _p(act),
+                                           _p(ws), ws.numel(), _stream()), "moe_grouped_gate_up_train")
+    return h13, act
+
+
+def grouped_down_grad(cfg, dy_perm, w2, h13, offsets, ws, dh13=None):
+    """dh13: the gradient through the down projection and SwiGLU (may be h13)."""
+    _product_args(cfg, offsets, ws, w2=w2)
+    _perm_arg(cfg, "dy_perm", dy_perm, cfg.H)
+    _perm_arg(cfg, "h13", h13, 2 * cfg.I)
+    dh13 = _rows_like(cfg, dy_perm, 2 * cfg.I, dh13)
+    _perm_arg(cfg, "dh13", dh13, 2 * cfg.I)
+    _check(lib().moe_grouped_down_grad(ctypes.byref(cfg), _p(dy_perm), _p(w2), _p(h13), _p(offsets), _p(dh13), _p(ws),
+                                       ws.numel(), _stream()), "moe_grouped_down_grad")
+    return dh13
+
+
+def grouped_gate_up_grad(cfg, dh13, w13, offsets, ws, dx_perm=None):
+    """dx_perm: the gradient through the gate/up projections."""
+    _product_args(cfg, offsets, ws, w13=w13)
+    _perm_arg(cfg, "dh13", dh13, 2 * cfg.I)
+    dx_perm = _rows_like(cfg, dh13, cfg.H, dx_perm)
+    _perm_arg(cfg, "dx_perm", dx_perm, cfg.H)
+    _check(lib().moe_grouped_gate_up_grad(ctypes.byref(cfg), _p(dh13), _p(w13), _p(offsets), _p(dx_perm), _p(ws),
+                                          ws.numel(), _stream()), "moe_grouped_gate_up_grad")
+    return dx_perm
+
+
+def grouped_down_wgrad(cfg, dy_perm, act, offsets, ws, dw2=None):
+    """dw2 [E, H, I] from the down projection's output gradient and its input."""
+    _product_args(cfg, offsets, ws)
+    _perm_arg(cfg, "dy_perm", dy_perm, cfg.H)
+    _perm_arg(cfg, "act", act, cfg.I)
+    if dw2 is None:
+        dw2 = torch.empty((cfg.E, cfg.H, cfg.I), dtype=act.dtype, device=act.device)
+    _arg("dw2", dw2, (cfg.E, cfg.H, cfg.I), _act_dtype(cfg))
+    _check(lib().moe_grouped_down_wgrad(ctypes.byref(cfg), _p(dy_perm), _p(act), _p(offsets), _p(dw2), _p(ws),
+                                        ws.numel(), _stream()), "moe_grouped_down_wgrad")
+    return dw2
+
+
+def grouped_gate_up_wgrad(cfg, dh13, x_perm, offsets, ws, dw13=None):
+    """dw13 [E, 2I, H] from the pre-activations' gradient and the permuted tokens."""
+    _product_args(cfg, offsets, ws)
+    _perm_arg(cfg, "dh13", dh13, 2 * cfg.I)
+    _perm_arg(cfg, "x_perm", x_perm, cfg.H)
+    if dw13 is None:
+        dw13 = torch.empty((cfg.E, 2 * cfg.I, cfg.H), dtype=x_perm.dtype, device=x_perm.device)
+    _arg("dw13", dw13, (cfg.E, 2 * cfg.I, cfg.H), _act_dtype(cfg))
+    _check(lib().moe_grouped_gate_up_wgrad(ctypes.byref(cfg), _p(dh13), _p(x_perm), _p(offsets), _p(dw13), _p(ws),
+                                           ws.numel(), _stream()), "moe_grouped_gate_up_wgrad")
+    return dw13

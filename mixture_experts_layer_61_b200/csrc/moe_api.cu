@@ -90,6 +90,37 @@ int check_cfg(const moe_config_t* c) {
     return MOE_OK;
 }
 
+int check_norm(const moe_norm_config_t* c) {
+    if (!c) return MOE_ERR_ARG;
+    const int eb = elt_bytes(c->dtype);
+    if (eb == 0 || c->T < 0 || c->T > (1 << 30) || c->H <= 0 || c->H % (16 / eb) != 0) return MOE_ERR_ARG;
+    if (c->gate_mode < 0 || c->gate_mode > 2) return MOE_ERR_ARG;
+    if (!(c->eps > 0.f) || !std::isfinite(c->eps) || !std::isfinite(c->res_scale)) return MOE_ERR_ARG;
+    if (!row_kernels_fit(c->H, c->dtype)) return MOE_ERR_ARG;
+    return MOE_OK;
+}
+
+// The tensors every form of the block norm takes: aligned, and there exactly
+// where the form needs them.
+int check_norm_args(const moe_norm_config_t* c, const void* y, const void* residual, const void* w_post,
+                    const void* gate, const void* w_next, const void* h, const void* n) {
+    if (!y && (!residual || w_post || c->gate_mode != 0)) return MOE_ERR_ARG;
+    if ((gate != nullptr) != (c->gate_mode != 0) || (n != nullptr) != (w_next != nullptr) || (!h && !n))
+        return MOE_ERR_ARG;
+    for (const void* p : {y, residual, w_post, gate, w_next, h, n})
+        if (!aligned16(p)) return MOE_ERR_ARG;
+    return MOE_OK;
+}
+
+// The training products' common checks: bf16, segments in whole MMA steps of
+// 16 rows (the weight gradients reduce over them).
+int check_train(const moe_config_t* cfg, const void* workspace) {
+    int rc = check_cfg(cfg);
+    if (rc) return rc;
+    if (cfg->dtype != 0 || cfg->tile_B % 16 != 0 || !workspace || !aligned16(workspace)) return MOE_ERR_ARG;
+    return MOE_OK;
+}
+
 long long p_max(const moe_config_t* c) {
     const long long A = (long long)c->T * c->K;
     if (c->pad_mode == 1) {
@@ -556,6 +587,201 @@ int moe_combine(const moe_config_t* cfg, const void* y_perm, const int32_t* pos,
         return MOE_ERR_ARG;
     return status_of(launch_combine(cfg->T, cfg->H, cfg->K, cfg->dtype, y_perm, pos, topk_w, shared_out, out,
                                     (cudaStream_t)stream));
+}
+
+int moe_combine_grad(const moe_config_t* cfg, const void* dout, const void* y_perm, const int32_t* pos,
+                     const float* topk_w, const int32_t* sorted_ids, const int32_t* scalars, void* dy_perm,
+                     float* dtopk_w, moe_stream_t stream) {
+    int rc = check_cfg(cfg);
+    if (rc) return rc;
+    if (!row_kernels_fit(cfg->H, cfg->dtype)) return MOE_ERR_ARG;
+    if (cfg->T == 0) return MOE_OK;
+    if (!dout || !y_perm || !pos || !topk_w || !sorted_ids || !scalars || !dy_perm || !dtopk_w) return MOE_ERR_ARG;
+    if (!aligned16(dout) || !aligned16(y_perm) || !aligned16(dy_perm)) return MOE_ERR_ARG;
+    CombineGradArgs a{cfg->T,  cfg->H, cfg->K, cfg->dtype, p_max(cfg), dout,    y_perm,
+                      pos,     topk_w, sorted_ids, scalars, dy_perm,    dtopk_w};
+    return status_of(launch_combine_grad(a, (cudaStream_t)stream));
+}
+
+int moe_permute_grad(const moe_config_t* cfg, const void* dx_perm, const int32_t* pos, const void* dx_add, void* dx,
+                     moe_stream_t stream) {
+    int rc = check_cfg(cfg);
+    if (rc) return rc;
+    if (cfg->T == 0) return MOE_OK;
+    if (!dx_perm || !pos || !dx || !aligned16(dx_perm) || !aligned16(dx) || !aligned16(dx_add)) return MOE_ERR_ARG;
+    DeviceInfo d;
+    if ((rc = current_device(&d)) != 0) return status_of(rc);
+    return status_of(launch_permute_grad(cfg->T, cfg->H, cfg->K, cfg->dtype, dx_perm, pos, dx_add, dx,
+                                         (cudaStream_t)stream));
+}
+
+int moe_route_grad(const moe_config_t* cfg, const float* logits, const int32_t* topk_ids, const float* dtopk_w,
+                   float* dlogits, moe_stream_t stream) {
+    int rc = check_cfg(cfg);
+    if (rc) return rc;
+    if (cfg->T == 0) return MOE_OK;
+    if (!logits || !topk_ids || !dtopk_w || !dlogits) return MOE_ERR_ARG;
+    DeviceInfo d;
+    if ((rc = current_device(&d)) != 0) return status_of(rc);
+    return status_of(launch_route_grad(cfg->T, cfg->E, cfg->K, cfg->score_fn, cfg->renorm, logits, topk_ids, dtopk_w,
+                                       dlogits, (cudaStream_t)stream));
+}
+
+int moe_block_norm(const moe_norm_config_t* nc, const void* y, const void* residual, const void* w_post,
+                   const void* gate, const void* w_next, void* h, void* n, moe_stream_t stream) {
+    int rc = check_norm(nc);
+    if (rc) return rc;
+    if (nc->T == 0) return MOE_OK;
+    if ((rc = check_norm_args(nc, y, residual, w_post, gate, w_next, h, n)) != 0) return rc;
+    DeviceInfo d;
+    if ((rc = current_device(&d)) != 0) return status_of(rc);
+    BlockNormArgs a{nc->T, nc->H, 0, nc->dtype, nc->gate_mode, nc->eps, nc->res_scale, y, nullptr, nullptr, nullptr,
+                    residual, w_post, gate, w_next, nullptr, h, n};
+    return status_of(launch_block_norm(a, (cudaStream_t)stream));
+}
+
+int moe_combine_norm(const moe_config_t* cfg, const moe_norm_config_t* nc, const void* y_perm, const int32_t* pos,
+                     const float* topk_w, const void* shared_out, const void* residual, const void* w_post,
+                     const void* gate, const void* w_next, void* y_out, void* h, void* n, moe_stream_t stream) {
+    int rc = check_cfg(cfg);
+    if (rc) return rc;
+    if ((rc = check_norm(nc)) != 0) return rc;
+    if (nc->T != cfg->T || nc->H != cfg->H || nc->dtype != cfg->dtype) return MOE_ERR_ARG;
+    if (cfg->T == 0) return MOE_OK;
+    if (!y_perm || !pos || !topk_w || !aligned16(shared_out) || !aligned16(y_out)) return MOE_ERR_ARG;
+    if ((rc = check_norm_args(nc, y_perm, residual, w_post, gate, w_next, h, n)) != 0) return rc;
+    DeviceInfo d;
+    if ((rc = current_device(&d)) != 0) return status_of(rc);
+    BlockNormArgs a{nc->T, nc->H, cfg->K, nc->dtype, nc->gate_mode, nc->eps, nc->res_scale, y_perm, pos, topk_w,
+                    shared_out, residual, w_post, gate, w_next, y_out, h, n};
+    return status_of(launch_block_norm(a, (cudaStream_t)stream));
+}
+
+size_t moe_block_norm_grad_workspace_size(const moe_norm_config_t* nc) {
+    if (check_norm(nc) != MOE_OK) return 0;
+    DeviceInfo d;
+    if (current_device(&d) != 0) return 0;
+    return align256((size_t)norm_grad_blocks(nc->T, d.num_sms) * 2 * nc->H * sizeof(float) + 1);
+}
+
+int moe_block_norm_grad(const moe_norm_config_t* nc, const void* h, const void* dh, const void* dn, const void* y,
+                        const void* w_post, const void* gate, const void* w_next, void* dresidual, void* dy,
+                        void* dgate, float* dw_post, float* dw_next, void* workspace, size_t ws_bytes,
+                        moe_stream_t stream) {
+    int rc = check_norm(nc);
+    if (rc) return rc;
+    // gradients come in for h, n or both; n's needs h and w_next
+    if ((dn != nullptr) != (w_next != nullptr) || (dw_next && !dn) || (dw_post && !w_post)) return MOE_ERR_ARG;
+    if ((gate != nullptr) != (nc->gate_mode != 0) || (dgate != nullptr) != (gate != nullptr)) return MOE_ERR_ARG;
+    if ((w_post || gate) && !(y || nc->T == 0)) return MOE_ERR_ARG;
+    if (nc->T > 0 && ((!dh && !dn) || (dn && !h) || (y != nullptr) != (dy != nullptr) || (!dresidual && !dy)))
+        return MOE_ERR_ARG;
+    for (const void* p : {h, dh, dn, y, w_post, gate, w_next, (const void*)dresidual, (const void*)dy,
+                          (const void*)dgate, (const void*)dw_post, (const void*)dw_next, (const void*)workspace})
+        if (!aligned16(p)) return MOE_ERR_ARG;
+    if (!workspace) return MOE_ERR_ARG;
+    DeviceInfo d;
+    if ((rc = current_device(&d)) != 0) return status_of(rc);
+    if (ws_bytes < (size_t)norm_grad_blocks(nc->T, d.num_sms) * 2 * nc->H * sizeof(float)) return MOE_ERR_WORKSPACE;
+    BlockNormGradArgs a{nc->T, nc->H, nc->dtype, nc->gate_mode, nc->eps, nc->res_scale, h, dh, dn, y, w_post, gate,
+                        w_next, dresidual, dy, dgate, dw_post, dw_next, static_cast<float*>(workspace)};
+    return status_of(launch_block_norm_grad(a, (cudaStream_t)stream));
+}
+
+int moe_grouped_gate_up_train(const moe_config_t* cfg, const void* x_perm, const void* w13, const int32_t* offsets,
+                              void* h13, void* act, void* workspace, size_t ws_bytes, moe_stream_t stream) {
+    int rc = check_train(cfg, workspace);
+    if (rc) return rc;
+    if (cfg->T == 0) return MOE_OK;
+    if (!x_perm || !w13 || !offsets || !h13 || !act) return MOE_ERR_ARG;
+    if (!aligned16(x_perm) || !aligned16(w13) || !aligned16(h13) || !aligned16(act)) return MOE_ERR_ARG;
+    DeviceInfo d;
+    if ((rc = current_device(&d)) != 0) return status_of(rc);
+    if (ws_bytes < ctl_block_bytes(d.num_sms)) return MOE_ERR_WORKSPACE;
+    GemmLaunch g = gate_up_launch(x_perm, p_max(cfg), offsets, cfg->E, 0, cfg->H, cfg->I, cfg->dtype, w13, act, 256);
+    g.pre = h13;
+    return status_of(launch_gemm_train(kTrainGateUp, g, gemm_ctl(workspace, d.num_sms), (cudaStream_t)stream));
+}
+
+int moe_grouped_down_grad(const moe_config_t* cfg, const void* dy_perm, const void* w2, const void* h13,
+                          const int32_t* offsets, void* dh13, void* workspace, size_t ws_bytes, moe_stream_t stream) {
+    int rc = check_train(cfg, workspace);
+    if (rc) return rc;
+    if (cfg->T == 0) return MOE_OK;
+    if (!dy_perm || !w2 || !h13 || !offsets || !dh13) return MOE_ERR_ARG;
+    if (!aligned16(dy_perm) || !aligned16(w2) || !aligned16(h13) || !aligned16(dh13)) return MOE_ERR_ARG;
+    DeviceInfo d;
+    if ((rc = current_device(&d)) != 0) return status_of(rc);
+    if (ws_bytes < ctl_block_bytes(d.num_sms)) return MOE_ERR_WORKSPACE;
+    GemmLaunch g{};
+    g.x = dy_perm;
+    g.x_rows = p_max(cfg);
+    g.w = w2;
+    g.kdim = cfg->H;
+    g.n_out = cfg->I;
+    g.seg_offsets = offsets;
+    g.n_groups = cfg->E;
+    g.out = dh13;
+    g.out_ld = 2 * cfg->I;
+    g.max_n = 256;
+    g.pre = const_cast<void*>(h13);
+    return status_of(launch_gemm_train(kTrainDownGrad, g, gemm_ctl(workspace, d.num_sms), (cudaStream_t)stream));
+}
+
+int moe_grouped_gate_up_grad(const moe_config_t* cfg, const void* dh13, const void* w13, const int32_t* offsets,
+                             void* dx_perm, void* workspace, size_t ws_bytes, moe_stream_t stream) {
+    int rc = check_train(cfg, workspace);
+    if (rc) return rc;
+    if (cfg->T == 0) return MOE_OK;
+    if (!dh13 || !w13 || !offsets || !dx_perm) return MOE_ERR_ARG;
+    if (!aligned16(dh13) || !aligned16(w13) || !aligned16(dx_perm)) return MOE_ERR_ARG;
+    DeviceInfo d;
+    if ((rc = current_device(&d)) != 0) return status_of(rc);
+    if (ws_bytes < ctl_block_bytes(d.num_sms)) return MOE_ERR_WORKSPACE;
+    GemmLaunch g{};
+    g.x = dh13;
+    g.x_rows = p_max(cfg);
+    g.w = w13;
+    g.kdim = 2 * cfg->I;
+    g.n_out = cfg->H;
+    g.seg_offsets = offsets;
+    g.n_groups = cfg->E;
+    g.out = dx_perm;
+    g.out_ld = cfg->H;
+    g.max_n = 256;
+    return status_of(launch_gemm_train(kTrainGateUpGrad, g, gemm_ctl(workspace, d.num_sms), (cudaStream_t)stream));
+}
+
+namespace {
+int wgrad(const moe_config_t* cfg, const void* d_rows, int m, const void* x_rows, int n, const int32_t* offsets,
+          void* out, void* workspace, size_t ws_bytes, moe_stream_t stream) {
+    int rc = check_train(cfg, workspace);
+    if (rc) return rc;
+    if (!out || !aligned16(out)) return MOE_ERR_ARG;
+    if (cfg->T > 0 && (!d_rows || !x_rows || !offsets || !aligned16(d_rows) || !aligned16(x_rows))) return MOE_ERR_ARG;
+    DeviceInfo d;
+    if ((rc = current_device(&d)) != 0) return status_of(rc);
+    if (ws_bytes < ctl_block_bytes(d.num_sms)) return MOE_ERR_WORKSPACE;
+    if (cfg->T == 0) {
+        const cudaError_t e = cudaMemsetAsync(out, 0, (size_t)2 * cfg->E * m * n, (cudaStream_t)stream);
+        if (e != cudaSuccess) cudaGetLastError();
+        return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
+    const WgradLaunch L{d_rows, x_rows, p_max(cfg), m, n, cfg->E, offsets, out};
+    return status_of(launch_wgrad(L, gemm_ctl(workspace, d.num_sms), (cudaStream_t)stream));
+}
+}  // namespace
+
+int moe_grouped_down_wgrad(const moe_config_t* cfg, const void* dy_perm, const void* act, const int32_t* offsets,
+                           void* dw2, void* workspace, size_t ws_bytes, moe_stream_t stream) {
+    if (!cfg) return MOE_ERR_ARG;
+    return wgrad(cfg, dy_perm, cfg->H, act, cfg->I, offsets, dw2, workspace, ws_bytes, stream);
+}
+
+int moe_grouped_gate_up_wgrad(const moe_config_t* cfg, const void* dh13, const void* x_perm, const int32_t* offsets,
+                              void* dw13, void* workspace, size_t ws_bytes, moe_stream_t stream) {
+    if (!cfg) return MOE_ERR_ARG;
+    return wgrad(cfg, dh13, 2 * cfg->I, x_perm, cfg->H, offsets, dw13, workspace, ws_bytes, stream);
 }
 
 int moe_layer_forward(const moe_config_t* cfg, const void* x, const void* w_router, const void* w13, const void* w2,

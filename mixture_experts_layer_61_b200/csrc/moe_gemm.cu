@@ -1,118 +1,14 @@
 // moe_gemm.cu -- host side of the tcgen05 grouped GEMM: TMA tensor maps,
 // variant dispatch (operand dtype, SwiGLU or plain epilogue, token-tile cap)
 // and the persistent launch.
-#include <mutex>
-
 #include "moe_ffn_stream.cuh"
 #include "moe_gemm.cuh"
+#include "moe_gemm_host.cuh"
 #include "moe_internal.h"
 
 namespace moe {
 
 namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-        cudaGetLastError();
-    });
-    return fn;
-}
-
-// [rows, kdim] row-major, box = box_rows x row_bytes (128 or 64) with the
-// swizzle of that width, out-of-range elements read as zero.
-bool make_map(CUtensorMap* m, CUtensorMapDataType dt, int elt_bytes, const void* base, long long rows, int kdim,
-              int box_rows, int row_bytes = 128) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {static_cast<cuuint64_t>(kdim), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(kdim) * elt_bytes};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(row_bytes / elt_bytes), static_cast<cuuint32_t>(box_rows)};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
-}
-
-template <typename T, typename OutT, int kEpi, int kMaxN, int kCta = 1>
-int launch_variant(const GemmLaunch& L, const GemmCtl& ctl, int num_sms, cudaStream_t stream) {
-    using C = GemmCfg<T, kEpi, kMaxN, kCta>;
-    auto kern = moe_gemm_kernel<T, OutT, kEpi, kMaxN, kCta>;
-    if (kCta == 2 && (num_sms & 1)) return -1;
-    static int grid_blocks = 0;  // per instantiation: CTAs that can be resident at once
-    static bool attr_done = false;  // per instantiation
-    if (!attr_done) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess) {
-            cudaGetLastError();
-            return -3;
-        }
-        grid_blocks = num_sms;
-        if (kCta > 1) {
-            // pairs must sit in one GPC: size the persistent grid by the clusters that fit
-            cudaLaunchConfig_t oc = {};
-            oc.gridDim = dim3(num_sms);
-            oc.blockDim = dim3(kGemmThreads);
-            oc.dynamicSmemBytes = C::kSmemBytes;
-            cudaLaunchAttribute ca;
-            ca.id = cudaLaunchAttributeClusterDimension;
-            ca.val.clusterDim.x = kCta;
-            ca.val.clusterDim.y = 1;
-            ca.val.clusterDim.z = 1;
-            oc.attrs = &ca;
-            oc.numAttrs = 1;
-            int nclusters = 0;
-            if (cudaOccupancyMaxActiveClusters(&nclusters, kern, &oc) != cudaSuccess || nclusters <= 0) {
-                cudaGetLastError();
-                return -3;
-            }
-            grid_blocks = nclusters * kCta < num_sms ? nclusters * kCta : num_sms;
-        }
-        attr_done = true;
-    }
-    CUtensorMap tm_w, tm_x, tm_x64, tm_xbig;
-    constexpr int rb = C::kRowBytes;
-    if (!make_map(&tm_w, Elt<T>::kTma, Elt<T>::kBytes, L.w, L.w_rows, L.kdim, 128, rb)) return -3;
-    if (!make_map(&tm_x, Elt<T>::kTma, Elt<T>::kBytes, L.x, L.x_rows, L.kdim, C::kXBoxRows, rb)) return -3;
-    if (!make_map(&tm_x64, Elt<T>::kTma, Elt<T>::kBytes, L.x, L.x_rows, L.kdim, C::kXBoxMid, rb)) return -3;
-    if (!make_map(&tm_xbig, Elt<T>::kTma, Elt<T>::kBytes, L.x, L.x_rows, L.kdim, kMaxN / kCta, rb)) return -3;
-    GemmParams p;
-    p.seg_offsets = L.seg_offsets;
-    p.n_groups = L.n_groups;
-    p.seg_rows = L.seg_rows;
-    p.n_out = L.n_out;
-    p.kdim = L.kdim;
-    p.w_group_stride = L.w_group_stride;
-    p.up_offset = L.up_offset;
-    p.out = L.out;
-    p.out_ld = L.out_ld;
-    p.counters = ctl.counters;
-    p.partials = ctl.partials;
-    p.status = ctl.status;
-    p.wait_limit_ns = wait_limit_ns();
-    p.withhold_first_load = take_withhold_flag();
-    p.sk_min_units = 4;
-    p.max_split = L.max_split > 0 ? L.max_split : 4;
-    p.split_tail = split_tail_mode();
-    int grid = grid_blocks;
-    if (L.sms > 0 && L.sms < grid) grid = L.sms >= 2 * kCta ? L.sms - L.sms % kCta : kCta;
-    cudaError_t e = launch_kernel_cluster(kern, dim3(grid), dim3(kGemmThreads), C::kSmemBytes, stream, kCta,
-                                          tm_w, tm_x, tm_x64, tm_xbig, p);
-    count_launch();
-    if (e != cudaSuccess) cudaGetLastError();
-    return e == cudaSuccess ? 0 : -3;
-}
 
 template <typename T, typename OutT, int kEpi>
 int dispatch_n(const GemmLaunch& L, const GemmCtl& ctl, int num_sms, cudaStream_t s) {

@@ -72,13 +72,22 @@ struct GemmParams {
     int sk_min_units;     // minimum k-iterations per stream-K block
     int max_split;        // stream-K: most blocks contributing to one tile
     int split_tail;       // 1: whole waves data-parallel, the last partial wave in aligned k-slices
+    void* pre;            // training epilogues: pre-activations [rows, 2 n_out], gate then up columns
 };
 
 // Epilogue kinds: one 128-row weight tile per stage (plain store); gate and
 // up tiles of the same 128 features (SwiGLU); two adjacent 128-feature
 // blocks sharing one token tile (wide plain store, 256 features per tile).
-constexpr int kEpiPlain = 0, kEpiSwiGLU = 1, kEpiWide = 2;
+// Training: kEpiSwiGLUTrain is the SwiGLU epilogue that also stores the
+// pre-activations; kEpiSwiGLUGrad takes the accumulator as the gradient of
+// the activation, reads the pre-activations (g, u) and stores the gradients
+// of both: dg = dact u silu'(g), du = dact silu(g).
+constexpr int kEpiPlain = 0, kEpiSwiGLU = 1, kEpiWide = 2, kEpiSwiGLUTrain = 3, kEpiSwiGLUGrad = 4;
 
+// Weights as the MMA's M operand: rows of output features, K contiguous
+// ([out, in] used forward: K-major), or for the gradients, which contract
+// over the weights' out axis, rows of K with the features contiguous
+// (MN-major).
 template <typename T, int kEpi, int kMaxN, int kCta = 1>
 struct GemmCfg {
     // Operand tiles are K-major rows of kRowBytes with the swizzle of that
@@ -89,7 +98,7 @@ struct GemmCfg {
     static constexpr int kBK = kRowBytes / Elt<T>::kBytes;  // K elements per stage
     static constexpr int kMmaK = 32 / Elt<T>::kBytes;       // K per MMA instruction
     static constexpr int kKSteps = kBK / kMmaK;             // MMAs per operand pair and stage
-    static constexpr int kNW = kEpi == kEpiPlain ? 1 : 2;  // weight tiles per stage
+    static constexpr int kNW = kEpi == kEpiPlain || kEpi == kEpiSwiGLUGrad ? 1 : 2;  // weight tiles per stage
     static constexpr int kFeat = kEpi == kEpiWide ? 256 : 128;  // output features per CTA and tile
     static constexpr int kFeatTile = kFeat * kCta;                 // output features per tile
     static constexpr int kUnit = 16 * kCta;                        // token-row granularity of the MMA
@@ -334,13 +343,14 @@ __device__ __forceinline__ void store_out<__nv_bfloat16>(__nv_bfloat16* ptr, flo
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 // ------------------------------------------------------------------ kernel
-template <typename T, typename OutT, int kEpi, int kMaxN, int kCta>
+template <typename T, typename OutT, int kEpi, int kMaxN, int kCta, bool kWMn = false>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                     const __grid_constant__ CUtensorMap tm_x64, const __grid_constant__ CUtensorMap tm_xbig,
                     const GemmParams p) {
     using C = GemmCfg<T, kEpi, kMaxN, kCta>;
-    constexpr bool kSwiGLU = kEpi == kEpiSwiGLU;
+    constexpr bool kSwiGLU = kEpi == kEpiSwiGLU || kEpi == kEpiSwiGLUTrain;
+    static_assert(!kWMn || (Elt<T>::kBytes == 2 && C::kBK == 64), "MN-major weights: 16-bit, 64 rows of K per box");
     constexpr bool kTwo = C::kNW == 2;
     constexpr bool kPair = kCta == 2;
     extern __shared__ uint8_t smem_raw[];
@@ -463,8 +473,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         if (kPair) tma_load_2d_pair(dst, m, fb, k * C::kBK, c1, pol);
                         else tma_load_2d(dst, m, &full[s], k * C::kBK, c1, pol);
                     };
-                    load(st, &tm_w, wrow, pol_w);
-                    if (kTwo) load(st + C::kWTileBytes, &tm_w, wrow + (kSwiGLU ? p.up_offset : 128), pol_w);
+                    if constexpr (kWMn) {
+                        // boxes of 64 features by kBK rows of K; K rows past kdim read as zero
+                        const int f0 = t.f0 + (int)rank * C::kFeat;
+#pragma unroll
+                        for (int b = 0; b < 2 * C::kNW; ++b) {
+                            if (kPair)
+                                tma_load_3d_pair(st + b * (C::kWTileBytes / 2), &tm_w, fb, f0 + 64 * b, k * C::kBK, t.group,
+                                                 pol_w);
+                            else
+                                tma_load_3d(st + b * (C::kWTileBytes / 2), &tm_w, &full[s], f0 + 64 * b, k * C::kBK,
+                                            t.group, pol_w);
+                        }
+                    } else {
+                        load(st, &tm_w, wrow, pol_w);
+                        if (kTwo) load(st + C::kWTileBytes, &tm_w, wrow + (kSwiGLU ? p.up_offset : 128), pol_w);
+                    }
                     uint8_t* xs = st + C::kNW * C::kWTileBytes;
                     int r = 0;
                     if (kMaxN / kCta > C::kXBoxMid && xn == kMaxN / kCta) {
@@ -505,7 +529,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 tc_fence_after();
                 const uint32_t d_gate = tmem_base + b * C::kAccCols;
                 const uint32_t d_up = d_gate + kMaxN;
-                const uint32_t idesc = umma_idesc(Elt<T>::kMmaFmt, 128 * kCta, t.mma_n);
+                const uint32_t idesc = umma_idesc(Elt<T>::kMmaFmt, 128 * kCta, t.mma_n) | (kWMn ? kIdescAMn : 0u);
                 for (int k = it.kb; k < it.ke; ++k, ++kc) {
                     const int s = kc % C::kStages;
                     const uint32_t ph = (kc / C::kStages) & 1u;
@@ -516,18 +540,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     tc_fence_after();
                     uint8_t* st = stage_base + s * C::kStageBytes;
                     auto desc = [](uint32_t a) { return C::kRowBytes == 128 ? umma_desc_sw128(a) : umma_desc_sw64(a); };
-                    const uint64_t a0 = desc(smem_u32(st));
-                    const uint64_t a1 = desc(smem_u32(st + C::kWTileBytes));
+                    auto wdesc = [desc](uint32_t a) { return kWMn ? umma_desc_mn_sw128<64>(a) : desc(a); };
+                    // K of one MMA: 32 bytes along a K-major row, 16 rows of 128 bytes in an MN-major box
+                    constexpr uint32_t kWStep = kWMn ? 16 * 128 / 16 : 2;
+                    const uint64_t a0 = wdesc(smem_u32(st));
+                    const uint64_t a1 = wdesc(smem_u32(st + C::kWTileBytes));
                     const uint64_t bx = desc(smem_u32(st + C::kNW * C::kWTileBytes));
 #pragma unroll
                     for (int kk = 0; kk < C::kKSteps; ++kk) {
                         const uint32_t acc = (k > it.kb || kk > 0) ? 1u : 0u;
                         if (kPair) {
-                            umma_pair_bf16(d_gate, a0 + 2 * kk, bx + 2 * kk, idesc, acc);
-                            if (kTwo) umma_pair_bf16(d_up, a1 + 2 * kk, bx + 2 * kk, idesc, acc);
+                            umma_pair_bf16(d_gate, a0 + kWStep * kk, bx + 2 * kk, idesc, acc);
+                            if (kTwo) umma_pair_bf16(d_up, a1 + kWStep * kk, bx + 2 * kk, idesc, acc);
                         } else {
-                            umma<T>(d_gate, a0 + 2 * kk, bx + 2 * kk, idesc, acc);
-                            if (kTwo) umma<T>(d_up, a1 + 2 * kk, bx + 2 * kk, idesc, acc);
+                            umma<T>(d_gate, a0 + kWStep * kk, bx + 2 * kk, idesc, acc);
+                            if (kTwo) umma<T>(d_up, a1 + kWStep * kk, bx + 2 * kk, idesc, acc);
                         }
                     }
                     if (kPair) {  // the stage is free in both CTAs
@@ -565,7 +592,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         constexpr int kCh = kHalfN >= 32 ? 32 : 16;
         constexpr bool kBf16Out = sizeof(OutT) == 2;
         constexpr int kRegs = kBf16Out ? kHalfN / 2 : kHalfN;  // packed results of one accumulator
-        constexpr bool kEarly = kEpi != kEpiWide && kRegs <= 64;
+        constexpr bool kEarly = (kEpi == kEpiPlain || kEpi == kEpiSwiGLU) && kRegs <= 64;
         const int cbeg = half * kHalfN;
         OutT* out = reinterpret_cast<OutT*>(p.out);
         uint32_t ac = 0;
@@ -618,8 +645,49 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             // (callers skip blocks that start past the last real column; whole
             // blocks store without per-element predicates, which measured
             // markedly faster than predicating every store)
-            auto emit = [orow, nrows, out_ld, v0, v1](int c0, float (&g)[16], float (&u)[16]) {
+            OutT* prow = nullptr;  // this feature's pre-activation column (training)
+            if constexpr (kEpi == kEpiSwiGLUTrain || kEpi == kEpiSwiGLUGrad)
+                prow = reinterpret_cast<OutT*>(p.pre) + (long long)t.row0 * 2 * p.n_out + f;
+            const int n_out = p.n_out;
+            auto emit = [orow, prow, n_out, nrows, out_ld, v0, v1](int c0, float (&g)[16], float (&u)[16]) {
                 const int n = nrows - c0 < 16 ? nrows - c0 : 16;
+                if constexpr (kEpi == kEpiSwiGLUTrain) {
+                    if (v0) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            if (i < n) {
+                                OutT* pr = prow + (long long)(c0 + i) * 2 * n_out;
+                                store_out<OutT>(pr, g[i]);
+                                store_out<OutT>(pr + n_out, u[i]);
+                                store_out<OutT>(orow + (c0 + i) * out_ld, silu_mul(g[i], u[i]));
+                            }
+                        }
+                    }
+                    return;
+                }
+                if constexpr (kEpi == kEpiSwiGLUGrad) {
+                    if (v0) {
+                        float pg[16], pu[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            if (i < n) {
+                                const OutT* pr = prow + (long long)(c0 + i) * 2 * n_out;
+                                pg[i] = Elt<OutT>::to_f(pr[0]);
+                                pu[i] = Elt<OutT>::to_f(pr[n_out]);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            if (i < n) {
+                                const float sg = __fdividef(1.f, 1.f + __expf(-pg[i]));
+                                OutT* o = orow + (c0 + i) * out_ld;
+                                store_out<OutT>(o, g[i] * pu[i] * sg * (1.f + pg[i] * (1.f - sg)));
+                                store_out<OutT>(o + n_out, g[i] * pg[i] * sg);
+                            }
+                        }
+                    }
+                    return;
+                }
                 if (n == 16) {
                     if (v0) {
 #pragma unroll
@@ -710,7 +778,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         for (int i = 0; i < 16; ++i) {
                             g[i] = __uint_as_float(ga[16 * h + i]);
                             u[i] = kTwo ? __uint_as_float(ua[16 * h + i]) : 0.f;
-                            if (kSwiGLU) g[i] = silu_mul(g[i], u[i]);
+                            if (kEpi == kEpiSwiGLU) g[i] = silu_mul(g[i], u[i]);
                         }
                         if (c0 + 16 * h < cend) emit(c0 + 16 * h, g, u);
                     }
@@ -815,7 +883,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                 }
                             }
                         }
-                        if (kSwiGLU) {
+                        if (kEpi == kEpiSwiGLU) {
 #pragma unroll
                             for (int i = 0; i < 16; ++i) g[i] = silu_mul(g[i], u[i]);
                         }

@@ -101,7 +101,27 @@ struct GemmLaunch {
     int max_n;                   // token-tile cap: 32, 64, 128 or 256
     int max_split;               // stream-K: most blocks per tile (0 = default 4)
     int sms;                     // persistent blocks at most (0 = one per SM): an SM share
+    void* pre;                   // training: pre-activations [x_rows, 2 n_out] (written forward, read backward)
 };
+
+// The products of a training step, bf16, on CTA pairs.
+// kTrainGateUp: w [n_groups, 2 n_out, kdim], act = silu(g) u into out, (g, u) into pre;
+// kTrainDownGrad: w [n_groups, kdim, n_out], x the gradient of the down
+// projection's output; out [x_rows, 2 n_out] the gradients of (g, u) read from pre;
+// kTrainGateUpGrad: w [n_groups, kdim, n_out], out = x w.
+enum TrainGemm { kTrainGateUp, kTrainDownGrad, kTrainGateUpGrad };
+int launch_gemm_train(TrainGemm kind, const GemmLaunch& L, const GemmCtl& ctl, cudaStream_t stream);
+// Weight gradients, bf16: out[g] [m, n] = sum over rows p of segment g of
+// d[p] (outer) x[p], for every group (zero without rows).
+struct WgradLaunch {
+    const void* d;
+    const void* x;
+    long long rows;  // of d [rows, m] and x [rows, n]
+    int m, n, n_groups;
+    const int32_t* seg_offsets;
+    void* out;
+};
+int launch_wgrad(const WgradLaunch& L, const GemmCtl& ctl, cudaStream_t stream);
 
 int launch_gemm(const GemmLaunch& L, const GemmCtl& ctl, cudaStream_t stream);
 
@@ -211,6 +231,55 @@ struct RouteCcArgs {
     int* done_ctr;
 };
 int launch_route_cc(const RouteCcArgs& a, cudaStream_t stream);
+
+// Rows the row-wise training kernels hold in registers (H * elt <= 32 KB).
+bool row_kernels_fit(int H, int dtype);
+// The norms around a block: see moe_block_norm / moe_combine_norm.  y is
+// [T, H], or with pos given the permuted expert rows the combine sums.
+struct BlockNormArgs {
+    int T, H, K, dtype, gate_mode;
+    float eps, res_scale;
+    const void* y;
+    const int32_t* pos;
+    const float* topk_w;
+    const void* shared_out;
+    const void* residual;
+    const void* w_post;
+    const void* gate;
+    const void* w_next;
+    void *y_out, *h, *n;
+};
+int launch_block_norm(const BlockNormArgs& a, cudaStream_t stream);
+// Blocks of the gradient kernel, each leaving 2 H fp32 column sums in `partials`.
+int norm_grad_blocks(int T, int num_sms);
+struct BlockNormGradArgs {
+    int T, H, dtype, gate_mode;
+    float eps, res_scale;
+    const void *h, *dh, *dn, *y;
+    const void *w_post, *gate, *w_next;
+    void *dresidual, *dy, *dgate;
+    float *dw_post, *dw_next, *partials;
+};
+int launch_block_norm_grad(const BlockNormGradArgs& a, cudaStream_t stream);
+// The combine's gradient: dy_perm (padding rows zeroed) and the gate weights'.
+struct CombineGradArgs {
+    int T, H, K, dtype;
+    long long P_max;
+    const void* dout;
+    const void* y_perm;
+    const int32_t* pos;
+    const float* topk_w;
+    const int32_t* sorted_ids;
+    const int32_t* scalars;
+    void* dy_perm;
+    float* dw;
+};
+int launch_combine_grad(const CombineGradArgs& a, cudaStream_t stream);
+int launch_route_grad(int T, int E, int K, int score_fn, int renorm, const float* logits, const int32_t* ids,
+                      const float* dw, float* dlogits, cudaStream_t stream);
+// The permute's gradient: the combine with unit weights.
+int launch_permute_grad(int T, int H, int K, int dtype, const void* dx_perm, const int32_t* pos, const void* dx_add,
+                        void* dx, cudaStream_t stream);
 
 // Row-wise FP8 E4M3 quantisation: q [rows, cols] codes, scales [rows].
 int launch_quantize_fp8(long long rows, int cols, int dtype, const void* w, uint8_t* q, float* scales,

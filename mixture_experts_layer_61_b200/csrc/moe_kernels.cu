@@ -8,6 +8,7 @@
 
 #include "moe_common.cuh"
 #include "moe_internal.h"
+#include "moe_vec.cuh"
 
 namespace moe {
 
@@ -1177,40 +1178,6 @@ int launch_split_e4m3(int H, int K, long long rows, const void* x, const int32_t
 
 // ---------------------------------------------------------------- combine
 // out[t] = sum_k w[t,k] * y_perm[pos[t*K+k]] (+ shared[t]), fp32, ascending k.
-template <typename T>
-struct Vec16 {
-    static constexpr int N = 16 / sizeof(T);
-};
-
-__device__ __forceinline__ void unpack(const int4& v, float* f, const __nv_bfloat16*) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 x = __bfloat1622float2(h[i]);
-        f[2 * i] = x.x;
-        f[2 * i + 1] = x.y;
-    }
-}
-__device__ __forceinline__ void unpack(const int4& v, float* f, const float*) {
-    const float* x = reinterpret_cast<const float*>(&v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = x[i];
-}
-__device__ __forceinline__ int4 pack(const float* f, const __nv_bfloat16*) {
-    int4 v;
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-    return v;
-}
-__device__ __forceinline__ int4 pack(const float* f, const float*) {
-    int4 v;
-    float* x = reinterpret_cast<float*>(&v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = f[i];
-    return v;
-}
-
 // Stores the N fp32 sums of one 16-byte input vector: rounded once to the
 // activation dtype, or (TP partials, which an all-reduce sums next) unrounded.
 template <int N>
@@ -1229,7 +1196,8 @@ __device__ __forceinline__ void store_sums(const float* acc, float* out) {
 // summed in fp32 in ascending k (empty slots skipped), the shared output added
 // last, one rounding.  The output holds the columns [col0, col0 + ncol) (in
 // 16-byte vectors of the input rows; ncol vectors per output row).
-template <typename T, typename TOut, int kMaxK>
+// kUnit: every weight 1 (the permute's gradient), w not read.
+template <typename T, typename TOut, int kMaxK, bool kUnit = false>
 __global__ void __launch_bounds__(256) combine_kernel(int T_, int row_vec, int K, int col0, int ncol,
                                                       const int4* __restrict__ y_perm,
                                                       const int32_t* __restrict__ pos, const float* __restrict__ w,
@@ -1260,7 +1228,7 @@ __global__ void __launch_bounds__(256) combine_kernel(int T_, int row_vec, int K
             if (k < K && p[k] >= 0) {  // empty slot (per-token dynamic K): skipped
                 float y[N];
                 unpack(yv[k], y, (const T*)nullptr);
-                const float wk = __ldg(w + t * K + k);
+                const float wk = kUnit ? 1.f : __ldg(w + t * K + k);
 #pragma unroll
                 for (int j = 0; j < N; ++j) acc[j] += wk * y[j];
             }
@@ -1311,6 +1279,35 @@ int launch_combine(int T, int H, int K, int dtype, const void* y_perm, const int
     else if (K <= 4) e = go(std::integral_constant<int, 4>());
     else if (K <= 8) e = go(std::integral_constant<int, 8>());
     else e = go(std::integral_constant<int, 16>());
+    count_launch();
+    return launched(e);
+}
+
+// ------------------------------------------------------ permute's gradient
+// dx[t] = sum_k dx_perm[pos[t*K+k]] (+ dx_add[t]): the combine with unit weights.
+int launch_permute_grad(int T, int H, int K, int dtype, const void* dx_perm, const int32_t* pos, const void* dx_add,
+                        void* dx, cudaStream_t stream) {
+    if (T == 0) return 0;
+    const int row_vec = H * (dtype == 0 ? 2 : 4) / 16;
+    const int threads = 256;
+    long long blocks = ((long long)T * row_vec + threads - 1) / threads;
+    if (blocks > 0x7fffffffLL) blocks = 0x7fffffffLL;
+    const int4* y4 = static_cast<const int4*>(dx_perm);
+    const int4* s4 = static_cast<const int4*>(dx_add);
+    const dim3 g((unsigned)blocks), b(threads);
+    auto go = [&](auto kmax) -> cudaError_t {
+        constexpr int kK = decltype(kmax)::value;
+        using bf = __nv_bfloat16;
+        if (dtype == 0)
+            return launch_kernel(combine_kernel<bf, bf, kK, true>, g, b, 0, stream, T, row_vec, K, 0, row_vec, y4, pos,
+                                 (const float*)nullptr, s4, static_cast<bf*>(dx));
+        return launch_kernel(combine_kernel<float, float, kK, true>, g, b, 0, stream, T, row_vec, K, 0, row_vec, y4,
+                             pos, (const float*)nullptr, s4, static_cast<float*>(dx));
+    };
+    const cudaError_t e = K <= 2   ? go(std::integral_constant<int, 2>())
+                          : K <= 4 ? go(std::integral_constant<int, 4>())
+                          : K <= 8 ? go(std::integral_constant<int, 8>())
+                                   : go(std::integral_constant<int, 16>());
     count_launch();
     return launched(e);
 }

@@ -1,0 +1,723 @@
+// moe_train.cu -- the row-wise operators of a training step around the
+// expert FFN: the gradients of the combine ("local sum"), of the permute and
+// of the top-K gate, and the norms before and after the block (with the
+// block's gate and residual scale, fused with the combine) with their
+// gradient.  All are bound by device memory at training sizes and by latency
+// at decode sizes: each makes one pass over its rows, held in registers, with
+// fp32 sums.
+#include <climits>
+#include <type_traits>
+
+#include "moe_common.cuh"
+#include "moe_internal.h"
+#include "moe_vec.cuh"
+
+namespace moe {
+
+namespace {
+
+int launched(cudaError_t e) {
+    count_launch();
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return -3;
+    }
+    return 0;
+}
+
+template <typename T>
+__device__ __forceinline__ void up(const int4& v, float* f) {
+    unpack(v, f, (const T*)nullptr);
+}
+template <typename T>
+__device__ __forceinline__ int4 down(const float* f) {
+    return pack(f, (const T*)nullptr);
+}
+
+// ------------------------------------------------------------ block sums
+// Eight sums over a warp in nine shuffles: each step halves the values a lane
+// holds and doubles the lanes behind each; lane l ends with the sum of value
+// l & 7.
+__device__ __forceinline__ float warp_sum8(const float (&v)[8], int lane) {
+    float a[4], b[2], c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool hi = lane & 4;
+        const float send = hi ? v[i] : v[i + 4];
+        a[i] = (hi ? v[i + 4] : v[i]) + __shfl_xor_sync(0xffffffffu, send, 4);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool hi = lane & 2;
+        const float send = hi ? a[i] : a[i + 2];
+        b[i] = (hi ? a[i + 2] : a[i]) + __shfl_xor_sync(0xffffffffu, send, 2);
+    }
+    {
+        const bool hi = lane & 1;
+        const float send = hi ? b[0] : b[1];
+        c = (hi ? b[1] : b[0]) + __shfl_xor_sync(0xffffffffu, send, 1);
+    }
+    c += __shfl_xor_sync(0xffffffffu, c, 8);
+    c += __shfl_xor_sync(0xffffffffu, c, 16);
+    return c;
+}
+
+// Eight sums over the block, given to every thread.  `buf` is [32][8] floats;
+// two calls may not share it without a barrier in between (callers alternate
+// two buffers, so one barrier per call is enough).
+__device__ __forceinline__ void block_sum8(float (&v)[8], float* buf) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    float c = warp_sum8(v, lane);
+    if (nw > 1) {
+        if (lane < 8) buf[warp * 8 + lane] = c;
+        __syncthreads();
+        c = 0.f;
+        for (int w = lane >> 3; w < nw; w += 4) c += buf[w * 8 + (lane & 7)];
+        c += __shfl_xor_sync(0xffffffffu, c, 8);
+        c += __shfl_xor_sync(0xffffffffu, c, 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, c, i);
+}
+
+__device__ __forceinline__ float block_sum(float v, float* buf) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (nw > 1) {
+        if (lane == 0) buf[warp] = v;
+        __syncthreads();
+        v = lane < nw ? buf[lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    }
+    return v;
+}
+
+constexpr int kRowThreads = 512;  // threads per block of the row kernels, at most
+
+// Vectors per thread (1, 2 or 4) and threads for rows of row_vec vectors:
+// one vector a thread while that needs at most 256 threads.
+void row_shape(int row_vec, int& kv, int& threads) {
+    kv = row_vec <= 256 ? 1 : (row_vec <= 2 * kRowThreads ? 2 : 4);
+    threads = (((row_vec + kv - 1) / kv) + 31) / 32 * 32;
+}
+
+}  // namespace
+
+bool row_kernels_fit(int H, int dtype) { return H * (dtype == 0 ? 2 : 4) / 16 <= 4 * kRowThreads; }
+
+// ------------------------------------------------------------- block norm
+// For one token:  y = the block's output (given, or the combine's weighted sum
+// of its K expert rows plus the shared output),
+//   z = y rsqrt(mean y^2 + eps) w_post   (y without a norm after the block)
+//   h = res_scale residual + gate z
+//   n = h rsqrt(mean h^2 + eps) w_next   (the norm before the next block)
+// One block per token, the row in registers as fp32 from the first load to
+// the last store, so every output is rounded once.
+template <typename T, int kV, int kMaxK>
+__global__ void __launch_bounds__(kRowThreads) block_norm_kernel(BlockNormArgs a) {
+    constexpr int N = Vec16<T>::N;
+    constexpr bool kCombine = kMaxK > 0;
+    __shared__ float red[2][32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int row_vec = a.H / N;
+    const long long t = blockIdx.x;
+    const long long base = t * row_vec;
+    const int4* res = static_cast<const int4*>(a.residual);
+    const int4* wpost = static_cast<const int4*>(a.w_post);
+    const int4* wnext = static_cast<const int4*>(a.w_next);
+    const int4* gate = static_cast<const int4*>(a.gate);
+    const long long gbase = a.gate_mode == 2 ? base : 0;
+    float y[kV][N];
+    int4 rv[kV];
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+        rv[j] = make_int4(0, 0, 0, 0);
+        if (res && v < row_vec) rv[j] = res[base + v];
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[j][i] = 0.f;
+    }
+    if constexpr (kCombine) {
+        const int4* yp = static_cast<const int4*>(a.y);
+        const int4* sh = static_cast<const int4*>(a.shared_out);
+        int p[kMaxK];
+        float w[kMaxK];
+#pragma unroll
+        for (int k = 0; k < kMaxK; ++k) {
+            p[k] = k < a.K ? __ldg(a.pos + t * a.K + k) : -1;
+            w[k] = k < a.K ? __ldg(a.topk_w + t * a.K + k) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            if (v < row_vec) {
+                int4 yv[kMaxK];
+                int4 sv = make_int4(0, 0, 0, 0);
+#pragma unroll
+                for (int k = 0; k < kMaxK; ++k)
+                    if (p[k] >= 0) yv[k] = __ldcs(yp + (long long)p[k] * row_vec + v);
+                if (sh) sv = __ldcs(sh + base + v);
+#pragma unroll
+                for (int k = 0; k < kMaxK; ++k) {
+                    if (p[k] >= 0) {  // empty slot (per-token dynamic K): skipped
+                        float f[N];
+                        up<T>(yv[k], f);
+#pragma unroll
+                        for (int i = 0; i < N; ++i) y[j][i] += w[k] * f[i];
+                    }
+                }
+                if (sh) {
+                    float f[N];
+                    up<T>(sv, f);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) y[j][i] += f[i];
+                }
+                if (a.y_out) static_cast<int4*>(a.y_out)[base + v] = down<T>(y[j]);
+            }
+        }
+    } else if (a.y) {
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            if (v < row_vec) up<T>(static_cast<const int4*>(a.y)[base + v], y[j]);
+        }
+    }
+    float r = 1.f;
+    if (wpost) {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < kV; ++j)
+#pragma unroll
+            for (int i = 0; i < N; ++i) s += y[j][i] * y[j][i];
+        r = rsqrtf(block_sum(s, red[0]) / a.H + a.eps);
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+        if (v < row_vec) {
+            float f[N];
+            if (wpost) {
+                up<T>(__ldg(wpost + v), f);
+#pragma unroll
+                for (int i = 0; i < N; ++i) y[j][i] *= r * f[i];
+            }
+            if (gate) {
+                up<T>(__ldg(gate + gbase + v), f);
+#pragma unroll
+                for (int i = 0; i < N; ++i) y[j][i] *= f[i];
+            }
+            up<T>(rv[j], f);
+            if (res) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) y[j][i] = fmaf(a.res_scale, f[i], y[j][i]);
+            }
+            if (a.h) static_cast<int4*>(a.h)[base + v] = down<T>(y[j]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) s += y[j][i] * y[j][i];
+        }
+    }
+    if (!wnext) return;
+    r = rsqrtf(block_sum(s, red[1]) / a.H + a.eps);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+        if (v < row_vec) {
+            float f[N];
+            up<T>(__ldg(wnext + v), f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) y[j][i] *= r * f[i];
+            static_cast<int4*>(a.n)[base + v] = down<T>(y[j]);
+        }
+    }
+}
+
+int launch_block_norm(const BlockNormArgs& a, cudaStream_t stream) {
+    if (a.T == 0) return 0;
+    int kv, threads;
+    row_shape(a.H * (a.dtype == 0 ? 2 : 4) / 16, kv, threads);
+    if (kv * kRowThreads * 16 < a.H * (a.dtype == 0 ? 2 : 4)) return -1;
+    const dim3 g((unsigned)a.T), b(threads);
+    cudaError_t e;
+    auto go = [&](auto tag, auto kvc, auto kmax) -> cudaError_t {
+        using E = typename std::remove_pointer<decltype(tag)>::type;
+        return launch_kernel(block_norm_kernel<E, decltype(kvc)::value, decltype(kmax)::value>, g, b, 0, stream, a);
+    };
+    auto go_k = [&](auto tag, auto kvc) -> cudaError_t {
+        if (!a.pos) return go(tag, kvc, std::integral_constant<int, 0>());
+        if (a.K <= 2) return go(tag, kvc, std::integral_constant<int, 2>());
+        if (a.K <= 8) return go(tag, kvc, std::integral_constant<int, 8>());
+        return go(tag, kvc, std::integral_constant<int, 16>());
+    };
+    auto go_v = [&](auto tag) -> cudaError_t {
+        if (kv == 1) return go_k(tag, std::integral_constant<int, 1>());
+        if (kv == 2) return go_k(tag, std::integral_constant<int, 2>());
+        return go_k(tag, std::integral_constant<int, 4>());
+    };
+    e = a.dtype == 0 ? go_v((__nv_bfloat16*)nullptr) : go_v((float*)nullptr);
+    return launched(e);
+}
+
+// ---------------------------------------------------- block norm's gradient
+// With rho_x = (mean x^2 + eps)^-1/2 and z, h, n as above:
+//   d    = dh + rho_h (w_next dn - h rho_h^2 mean(w_next dn h))   (h's whole gradient)
+//   dres = res_scale d;   dz = gate d;   dgate = d z (summed over the tokens for a channel gate)
+//   dy   = rho_y (w_post dz - y rho_y^2 mean(w_post dz y))
+//   dw_next = sum_t dn h rho_h;   dw_post = sum_t dz y rho_y
+// The second mean is a linear function of d, so with
+//   mean(w_post gate d y) = S(dh) + rho_h S(w_next dn) - rho_h^3 mean(w_next dn h) S(h),
+//   S(x) = mean(w_post gate x y)
+// six sums taken in one round give both means: one barrier per token.
+// For a channel gate both dw_post and dgate are products of one column sum,
+// A = sum_t d y rho_y (dw_post = gate A, dgate = w_post A).
+// Persistent blocks take tokens block-stride; the column sums stay in
+// registers over a block's tokens, go to the workspace as one fp32 row per
+// block and are added in block order by norm_wgrad_kernel: deterministic.
+template <typename T, int kV>
+__global__ void __launch_bounds__(kRowThreads) block_norm_grad_kernel(BlockNormGradArgs a) {
+    constexpr int N = Vec16<T>::N;
+    __shared__ float red[2][32 * 8];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int row_vec = a.H / N;
+    const int4* wpost = static_cast<const int4*>(a.w_post);
+    const int4* wnext = static_cast<const int4*>(a.w_next);
+    const int4* gate = static_cast<const int4*>(a.gate);
+    const int4 zero = make_int4(0, 0, 0, 0);
+    const float inv_h = 1.f / a.H;
+    float acc_next[kV][N], acc_post[kV][N];
+#pragma unroll
+    for (int j = 0; j < kV; ++j)
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc_next[j][i] = acc_post[j][i] = 0.f;
+    auto load = [&](const void* p, long long i) { return p ? __ldcs(static_cast<const int4*>(p) + i) : zero; };
+    int4 yv[kV], hv[kV], dhv[kV], dnv[kV];
+    auto load_row = [&](long long t) {
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            const bool in = v < row_vec;
+            const long long i = t * row_vec + v;
+            yv[j] = in ? load(a.y, i) : zero;
+            dhv[j] = in ? load(a.dh, i) : zero;
+            hv[j] = in && wnext ? load(a.h, i) : zero;
+            dnv[j] = in && wnext ? load(a.dn, i) : zero;
+        }
+    };
+    if (blockIdx.x < a.T) load_row(blockIdx.x);
+    int phase = 0;
+    for (long long t = blockIdx.x; t < a.T; t += gridDim.x, phase ^= 1) {
+        const long long gbase = a.gate_mode == 2 ? t * row_vec : 0;
+        float s[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            if (v < row_vec) {
+                float y[N], h[N], dh[N], dn[N], c[N], f[N];
+                up<T>(yv[j], y);
+                up<T>(hv[j], h);
+                up<T>(dhv[j], dh);
+                up<T>(dnv[j], dn);
+#pragma unroll
+                for (int i = 0; i < N; ++i) c[i] = 1.f;
+                if (wpost) up<T>(__ldg(wpost + v), c);
+                if (gate) {
+                    up<T>(__ldg(gate + gbase + v), f);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) c[i] *= f[i];
+                }
+                if (wnext) {
+                    up<T>(__ldg(wnext + v), f);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) dn[i] *= f[i];
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float cy = c[i] * y[i];
+                    s[0] += h[i] * h[i];
+                    s[1] += dn[i] * h[i];
+                    s[2] += y[i] * y[i];
+                    s[3] += cy * dh[i];
+                    s[4] += cy * dn[i];
+                    s[5] += cy * h[i];
+                }
+            }
+        }
+        block_sum8(s, red[phase]);
+        const float rh = wnext ? rsqrtf(s[0] * inv_h + a.eps) : 0.f;
+        const float mh = s[1] * inv_h * rh * rh * rh;  // h's coefficient in d
+        const float ry = wpost ? rsqrtf(s[2] * inv_h + a.eps) : 1.f;
+        const float my = wpost ? (s[3] + rh * s[4] - mh * s[5]) * inv_h * ry * ry * ry : 0.f;
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            const int v = threadIdx.x + j * blockDim.x;
+            if (v < row_vec) {
+                const long long o = t * row_vec + v;
+                float y[N], h[N], d[N], dn[N], f[N], g[N];
+                up<T>(yv[j], y);
+                up<T>(hv[j], h);
+                up<T>(dhv[j], d);
+                up<T>(dnv[j], dn);
+                if (wnext) {
+                    up<T>(__ldg(wnext + v), f);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        acc_next[j][i] += dn[i] * h[i] * rh;
+                        d[i] += rh * f[i] * dn[i] - mh * h[i];
+                    }
+                }
+                if (a.dresidual) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) f[i] = a.res_scale * d[i];
+                    static_cast<int4*>(a.dresidual)[o] = down<T>(f);
+                }
+                if (a.y) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) f[i] = g[i] = 1.f;
+                    if (wpost) up<T>(__ldg(wpost + v), f);
+                    if (gate) up<T>(__ldg(gate + gbase + v), g);
+                    if (a.gate_mode == 2) {
+                        float dg[N];
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            dg[i] = d[i] * y[i] * ry * f[i];
+                            acc_post[j][i] += g[i] * d[i] * y[i] * ry;
+                        }
+                        static_cast<int4*>(a.dgate)[o] = down<T>(dg);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < N; ++i) acc_post[j][i] += d[i] * y[i] * ry;
+                    }
+#pragma unroll
+                    for (int i = 0; i < N; ++i) f[i] = ry * f[i] * g[i] * d[i] - my * y[i];
+                    static_cast<int4*>(a.dy)[o] = down<T>(f);
+                }
+            }
+        }
+        if (t + gridDim.x < a.T) load_row(t + gridDim.x);
+    }
+    // one fp32 row per block: [gridDim.x][2][H]
+    float* part = a.partials + (long long)blockIdx.x * 2 * a.H;
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+        if (v < row_vec) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                if (wnext)
+                    *reinterpret_cast<float4*>(part + (long long)v * N + i) =
+                        make_float4(acc_next[j][i], acc_next[j][i + 1], acc_next[j][i + 2], acc_next[j][i + 3]);
+                if (a.y)
+                    *reinterpret_cast<float4*>(part + a.H + (long long)v * N + i) =
+                        make_float4(acc_post[j][i], acc_post[j][i + 1], acc_post[j][i + 2], acc_post[j][i + 3]);
+            }
+        }
+    }
+}
+
+// The blocks' column sums added in block order: 8 groups of rows per block,
+// then the groups in order.  blockIdx.y 0: dw_next; 1: dw_post and, for a
+// channel gate, dgate.
+template <typename T>
+__global__ void __launch_bounds__(256) norm_wgrad_kernel(BlockNormGradArgs a, int n_parts) {
+    __shared__ float4 sum[8][32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
+    const int c = (blockIdx.x * 32 + lane) * 4;
+    const bool post = blockIdx.y == 1;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c < a.H) {
+        const float* p = a.partials + (post ? a.H : 0) + c;
+        const int per = (n_parts + 7) / 8;
+        const int end = min(n_parts, (grp + 1) * per);
+#pragma unroll 8
+        for (int r = grp * per; r < end; ++r) {
+            const float4 v = __ldcs(reinterpret_cast<const float4*>(p + (long long)r * 2 * a.H));
+            s.x += v.x;
+            s.y += v.y;
+            s.z += v.z;
+            s.w += v.w;
+        }
+    }
+    sum[grp][lane] = s;
+    __syncthreads();
+    if (grp != 0 || c >= a.H) return;
+#pragma unroll
+    for (int g = 1; g < 8; ++g) {
+        const float4 v = sum[g][lane];
+        s.x += v.x;
+        s.y += v.y;
+        s.z += v.z;
+        s.w += v.w;
+    }
+    if (!post) {
+        if (a.dw_next) *reinterpret_cast<float4*>(a.dw_next + c) = s;
+        return;
+    }
+    const float f[4] = {s.x, s.y, s.z, s.w};
+    const T* g = static_cast<const T*>(a.gate);
+    const T* w = static_cast<const T*>(a.w_post);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (a.dw_post) a.dw_post[c + i] = a.gate_mode == 1 ? Elt<T>::to_f(g[c + i]) * f[i] : f[i];
+        if (a.gate_mode == 1 && a.dgate)
+            static_cast<float*>(a.dgate)[c + i] = w ? Elt<T>::to_f(w[c + i]) * f[i] : f[i];
+    }
+}
+
+int norm_grad_blocks(int T, int num_sms) { return T < num_sms ? T : num_sms; }
+
+int launch_block_norm_grad(const BlockNormGradArgs& a, cudaStream_t stream) {
+    DeviceInfo d;
+    int rc = current_device(&d);
+    if (rc != 0) return rc;
+    int kv, threads;
+    row_shape(a.H * (a.dtype == 0 ? 2 : 4) / 16, kv, threads);
+    if (kv * kRowThreads * 16 < a.H * (a.dtype == 0 ? 2 : 4)) return -1;
+    const int blocks = norm_grad_blocks(a.T, d.num_sms);
+    if (blocks > 0) {
+        const dim3 g(blocks), b(threads);
+        cudaError_t e;
+        auto go = [&](auto tag) -> cudaError_t {
+            using E = typename std::remove_pointer<decltype(tag)>::type;
+            if (kv == 1) return launch_kernel(block_norm_grad_kernel<E, 1>, g, b, 0, stream, a);
+            if (kv == 2) return launch_kernel(block_norm_grad_kernel<E, 2>, g, b, 0, stream, a);
+            return launch_kernel(block_norm_grad_kernel<E, 4>, g, b, 0, stream, a);
+        };
+        e = a.dtype == 0 ? go((__nv_bfloat16*)nullptr) : go((float*)nullptr);
+        if ((rc = launched(e)) != 0) return rc;
+    }
+    const bool post = a.dw_post || (a.dgate && a.gate_mode == 1);
+    if (!a.dw_next && !post) return 0;
+    const dim3 g((a.H / 4 + 31) / 32, post ? 2 : 1);
+    return launched(a.dtype == 0
+                        ? launch_kernel(norm_wgrad_kernel<__nv_bfloat16>, g, dim3(256), 0, stream, a, blocks)
+                        : launch_kernel(norm_wgrad_kernel<float>, g, dim3(256), 0, stream, a, blocks));
+}
+
+// ------------------------------------------------------ combine's gradient
+// dy_perm[pos(t,k)] = w(t,k) dout[t];  dw(t,k) = <dout[t], y_perm[pos(t,k)]>.
+// One block per token: dout's row is read once into registers and meets the K
+// rows it scales and is dotted with.  The blocks past the tokens zero the
+// padding rows (the weight gradients multiply them).
+template <typename T, int kV, int kMaxK>
+__global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(CombineGradArgs a) {
+    constexpr int N = Vec16<T>::N;
+    __shared__ float red[kMaxK][32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int row_vec = a.H / N;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    int4* dy = static_cast<int4*>(a.dy_perm);
+    if (blockIdx.x >= (unsigned)a.T) {
+        const int P = a.scalars[0];
+        const long long nwarps = (long long)(gridDim.x - a.T) * nw;
+        for (long long p0 = ((long long)(blockIdx.x - a.T) * nw + warp) * 32; p0 < P; p0 += nwarps * 32) {
+            const bool pad = p0 + lane < P && __ldg(a.sorted_ids + p0 + lane) < 0;
+            unsigned m = __ballot_sync(0xffffffffu, pad);
+            while (m) {
+                const long long p = p0 + __ffs(m) - 1;
+                m &= m - 1;
+                for (int v = lane; v < row_vec; v += 32) dy[p * row_vec + v] = make_int4(0, 0, 0, 0);
+            }
+        }
+        return;
+    }
+    const long long t = blockIdx.x;
+    float d[kV][N];
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+        const int v = threadIdx.x + j * blockDim.x;
+        int4 x = make_int4(0, 0, 0, 0);
+        if (v < row_vec) x = __ldcs(static_cast<const int4*>(a.dout) + t * row_vec + v);
+        up<T>(x, d[j]);
+    }
+    // kB rows requested before the first is used: dy_perm may be y_perm, so no
+    // load can move above an earlier row's store by itself
+    constexpr int kB = kMaxK < 8 / kV ? kMaxK : 8 / kV;
+    float dot[kMaxK];
+#pragma unroll
+    for (int k0 = 0; k0 < kMaxK; k0 += kB) {
+        int p[kB];
+        float w[kB];
+        int4 yv[kB][kV];
+#pragma unroll
+        for (int b = 0; b < kB; ++b) {
+            p[b] = k0 + b < a.K ? __ldg(a.pos + t * a.K + k0 + b) : -1;
+            w[b] = k0 + b < a.K ? __ldg(a.topk_w + t * a.K + k0 + b) : 0.f;
+        }
+#pragma unroll
+        for (int b = 0; b < kB; ++b)
+#pragma unroll
+            for (int j = 0; j < kV; ++j) {
+                const int v = threadIdx.x + j * blockDim.x;
+                if (p[b] >= 0 && v < row_vec)
+                    yv[b][j] = __ldcs(static_cast<const int4*>(a.y_perm) + (long long)p[b] * row_vec + v);
+            }
+#pragma unroll
+        for (int b = 0; b < kB; ++b) {
+            dot[k0 + b] = 0.f;
+            if (p[b] >= 0) {
+#pragma unroll
+                for (int j = 0; j < kV; ++j) {
+                    const int v = threadIdx.x + j * blockDim.x;
+                    if (v < row_vec) {
+                        float f[N];
+                        up<T>(yv[b][j], f);
+#pragma unroll
+                        for (int i = 0; i < N; ++i) {
+                            dot[k0 + b] += d[j][i] * f[i];
+                            f[i] = w[b] * d[j][i];
+                        }
+                        dy[(long long)p[b] * row_vec + v] = down<T>(f);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kMaxK; ++k) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot[k] += __shfl_xor_sync(0xffffffffu, dot[k], o);
+        if (lane == 0) red[k][warp] = dot[k];
+    }
+    __syncthreads();
+    for (int k = warp; k < a.K; k += nw) {
+        float s = lane < nw ? red[k][lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (lane == 0) a.dw[t * a.K + k] = s;
+    }
+}
+
+int launch_combine_grad(const CombineGradArgs& a, cudaStream_t stream) {
+    DeviceInfo d;
+    int rc = current_device(&d);
+    if (rc != 0) return rc;
+    int kv, threads;
+    row_shape(a.H * (a.dtype == 0 ? 2 : 4) / 16, kv, threads);
+    if (kv * kRowThreads * 16 < a.H * (a.dtype == 0 ? 2 : 4)) return -1;
+    // padding rows: a warp looks at 32 slots at a time
+    const long long pad_warps = (a.P_max + 31) / 32;
+    long long pad_blocks = (pad_warps + threads / 32 - 1) / (threads / 32);
+    if (pad_blocks > 4LL * d.num_sms) pad_blocks = 4LL * d.num_sms;
+    if (a.T + pad_blocks > INT_MAX) return -1;
+    const dim3 g((unsigned)(a.T + pad_blocks)), b(threads);
+    auto go = [&](auto tag, auto kvc, auto kmax) -> cudaError_t {
+        using E = typename std::remove_pointer<decltype(tag)>::type;
+        return launch_kernel(combine_grad_kernel<E, decltype(kvc)::value, decltype(kmax)::value>, g, b, 0, stream, a);
+    };
+    auto go_k = [&](auto tag, auto kvc) -> cudaError_t {
+        if (a.K <= 2) return go(tag, kvc, std::integral_constant<int, 2>());
+        if (a.K <= 8) return go(tag, kvc, std::integral_constant<int, 8>());
+        return go(tag, kvc, std::integral_constant<int, 16>());
+    };
+    auto go_v = [&](auto tag) -> cudaError_t {
+        if (kv == 1) return go_k(tag, std::integral_constant<int, 1>());
+        if (kv == 2) return go_k(tag, std::integral_constant<int, 2>());
+        return go_k(tag, std::integral_constant<int, 4>());
+    };
+    return launched(a.dtype == 0 ? go_v((__nv_bfloat16*)nullptr) : go_v((float*)nullptr));
+}
+
+// --------------------------------------------------------- gate's gradient
+// One warp per token; lane j < K holds slot j's expert, logit and weight
+// gradient.  With w the gate weights, p the full softmax, s the sigmoid:
+//   softmax, renormalised: dl_i = w_i (dw_i - sum_j w_j dw_j) on the selected
+//   softmax over all E:    dl_e = p_e (dw_e [e selected] - sum_j p_j dw_j)
+//   sigmoid, renormalised: dl_i = w_i (1 - s_i) (dw_i - sum_j w_j dw_j)
+//   sigmoid:               dl_i = s_i (1 - s_i) dw_i
+// 1 - s is taken as the sigmoid of -l, so it keeps its digits near s = 1.
+// The row is zeroed (or given the full softmax's share), then the selected
+// entries are written; a repeated expert's shares are added first.
+__global__ void __launch_bounds__(256) route_grad_kernel(int T, int E, int K, int score_fn, int renorm,
+                                                         const float* __restrict__ logits,
+                                                         const int32_t* __restrict__ ids,
+                                                         const float* __restrict__ dw, float* __restrict__ dlogits) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const long long t = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int lane = threadIdx.x & 31;
+    if (t >= T) return;
+    const float* l = logits + t * E;
+    float* out = dlogits + t * E;
+    auto wsum = [](float v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+        return v;
+    };
+    auto wmax = [](float v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+        return v;
+    };
+    const int id = lane < K ? ids[t * K + lane] : -1;
+    const bool on = id >= 0 && id < E;  // an empty slot has no gradient
+    const float li = on ? l[id] : 0.f;
+    const float di = on ? dw[t * K + lane] : 0.f;
+    const bool full = score_fn == 0 && !renorm;
+    float g;
+    if (score_fn == 0) {
+        float m = -INFINITY, den;
+        if (full) {
+            for (int e = lane; e < E; e += 32) m = fmaxf(m, l[e]);
+            m = wmax(m);
+            den = 0.f;
+            for (int e = lane; e < E; e += 32) den += expf(l[e] - m);
+            den = wsum(den);
+        } else {
+            m = wmax(on ? li : -INFINITY);
+            den = wsum(on ? expf(li - m) : 0.f);
+        }
+        const float w = on ? expf(li - m) / den : 0.f;
+        const float mean = wsum(w * di);
+        g = full ? w * di : w * (di - mean);
+        for (int e = lane; e < E; e += 32) out[e] = full ? -(expf(l[e] - m) / den) * mean : 0.f;
+        if (full) {
+            // the selected entries: their share of the row plus their own (shares of a repeated expert added below)
+            float own = 0.f;
+            for (int j = 0; j < K; ++j) {
+                const int ij = __shfl_sync(0xffffffffu, on ? id : -1, j);
+                const float gj = __shfl_sync(0xffffffffu, g, j);
+                if (ij == id) own += gj;
+            }
+            __syncwarp();
+            if (on) out[id] = own - w * mean;
+            return;
+        }
+    } else {
+        const float s = on ? 1.f / (1.f + expf(-li)) : 0.f;
+        const float c = 1.f / (1.f + expf(li));  // 1 - s
+        if (renorm) {
+            const float den = wsum(s);
+            const float w = on ? s / den : 0.f;
+            g = w * c * (di - wsum(w * di));
+        } else {
+            g = s * c * di;
+        }
+        for (int e = lane; e < E; e += 32) out[e] = 0.f;
+    }
+    float own = 0.f;
+    for (int j = 0; j < K; ++j) {
+        const int ij = __shfl_sync(0xffffffffu, on ? id : -1, j);
+        const float gj = __shfl_sync(0xffffffffu, g, j);
+        if (ij == id) own += gj;
+    }
+    __syncwarp();  // the zeros are written before the selected entries
+    if (on) out[id] = own;
+}
+
+int launch_route_grad(int T, int E, int K, int score_fn, int renorm, const float* logits, const int32_t* ids,
+                      const float* dw, float* dlogits, cudaStream_t stream) {
+    const int warps = 4;
+    return launched(launch_kernel(route_grad_kernel, dim3((unsigned)((T + warps - 1) / warps)), dim3(32 * warps), 0,
+                                  stream, T, E, K, score_fn, renorm, logits, ids, dw, dlogits));
+}
+
+}  // namespace moe
