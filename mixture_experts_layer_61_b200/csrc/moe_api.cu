@@ -670,12 +670,17 @@ int moe_block_norm_grad(const moe_norm_config_t* nc, const void* h, const void* 
                         moe_stream_t stream) {
     int rc = check_norm(nc);
     if (rc) return rc;
-    // gradients come in for h, n or both; n's needs h and w_next
-    if ((dn != nullptr) != (w_next != nullptr) || (dw_next && !dn) || (dw_post && !w_post)) return MOE_ERR_ARG;
-    if ((gate != nullptr) != (nc->gate_mode != 0) || (dgate != nullptr) != (gate != nullptr)) return MOE_ERR_ARG;
-    if ((w_post || gate) && !(y || nc->T == 0)) return MOE_ERR_ARG;
-    if (nc->T > 0 && ((!dh && !dn) || (dn && !h) || (y != nullptr) != (dy != nullptr) || (!dresidual && !dy)))
-        return MOE_ERR_ARG;
+    const bool rows = nc->T > 0;  // without tokens the row tensors may be NULL
+    const bool grow = nc->gate_mode == 2;
+    if ((dw_next && !w_next) || (dw_post && !w_post)) return MOE_ERR_ARG;
+    if (rows || !grow) {
+        if ((gate != nullptr) != (nc->gate_mode != 0) || (dgate != nullptr) != (gate != nullptr)) return MOE_ERR_ARG;
+    }
+    if (rows) {
+        // gradients come in for h, n or both; n's needs h and w_next
+        if ((dn != nullptr) != (w_next != nullptr) || (!dh && !dn) || (dn && !h)) return MOE_ERR_ARG;
+        if ((y != nullptr) != (dy != nullptr) || (!dresidual && !dy) || ((w_post || gate) && !y)) return MOE_ERR_ARG;
+    }
     for (const void* p : {h, dh, dn, y, w_post, gate, w_next, (const void*)dresidual, (const void*)dy,
                           (const void*)dgate, (const void*)dw_post, (const void*)dw_next, (const void*)workspace})
         if (!aligned16(p)) return MOE_ERR_ARG;
