@@ -72,6 +72,7 @@ struct GemmParams {
     int sk_min_units;     // minimum k-iterations per stream-K block
     int max_split;        // stream-K: most blocks contributing to one tile
     int split_tail;       // 1: whole waves data-parallel, the last partial wave in aligned k-slices
+    int w_joined;         // MN-major weights: tm_w loads a stage's weight tiles in one copy
     void* pre;            // training epilogues: pre-activations [rows, 2 n_out], gate then up columns
 };
 
@@ -112,10 +113,15 @@ struct GemmCfg {
     static constexpr int kTableBytes = 2 * (kMaxGroups + 1) * 4;
     static constexpr int kMiscBytes = 512;
     static constexpr int kMaxStages = 16;
-    static constexpr int kBudget = 227 * 1024 - 1024 - kTableBytes - kMiscBytes;
+    // kEpiSwiGLUGrad: each epilogue warp's pre-activations, kPreBufs blocks of
+    // (gate, up) x 16 tokens x 32 features, read ahead of the block in hand
+    static constexpr int kPreBufs = 3;
+    static constexpr int kPreBlockBytes = 2 * 16 * 32 * Elt<T>::kBytes;
+    static constexpr int kPreBytes = kEpi == kEpiSwiGLUGrad ? kGemmEpiWarps * kPreBufs * kPreBlockBytes : 0;
+    static constexpr int kBudget = 227 * 1024 - 1024 - kTableBytes - kMiscBytes - kPreBytes;
     static constexpr int kStagesRaw = kBudget / kStageBytes;
     static constexpr int kStages = kStagesRaw > kMaxStages ? kMaxStages : kStagesRaw;
-    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kTableBytes + kMiscBytes;
+    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kPreBytes + kTableBytes + kMiscBytes;
     static_assert(kStages >= 2, "pipeline needs two stages");
     static_assert(kMaxN % kUnit == 0 && kMaxN >= kUnit && kMaxN <= 256, "MMA N range");
     static_assert(kCta == 1 || kCta == 2, "one CTA or a CTA pair");
@@ -352,11 +358,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     constexpr bool kSwiGLU = kEpi == kEpiSwiGLU || kEpi == kEpiSwiGLUTrain;
     static_assert(!kWMn || (Elt<T>::kBytes == 2 && C::kBK == 64), "MN-major weights: 16-bit, 64 rows of K per box");
     constexpr bool kTwo = C::kNW == 2;
+    constexpr bool kTrain = kWMn || kEpi == kEpiSwiGLUTrain;
     constexpr bool kPair = kCta == 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* stage_base = smem;
-    int* seg = reinterpret_cast<int*>(smem + C::kStages * C::kStageBytes);
+    uint8_t* pre_base = smem + C::kStages * C::kStageBytes;
+    int* seg = reinterpret_cast<int*>(pre_base + C::kPreBytes);
     int* cbase = seg + (kMaxGroups + 1);
     uint8_t* misc = reinterpret_cast<uint8_t*>(cbase + (kMaxGroups + 1));
     uint64_t* full = reinterpret_cast<uint64_t*>(misc);
@@ -385,7 +393,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         for (int b = 0; b < C::kNumAcc; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 32 * kGemmEpiWarps * kCta);
+            mbar_init(&tempty[b], kGemmEpiWarps * kCta);
         }
         mbar_init(drain_bar, 1);
         fence_barrier_init();
@@ -452,8 +460,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const int wrow = t.wrow + (int)rank * C::kFeat;
                 const int xn = t.mma_n / kCta;
                 const int xrow = t.row0 + (int)rank * xn;
+                // Training variants load the token rows as one box, the smallest of the
+                // three that holds them (rows past the chunk are not multiplied): the
+                // issuing thread takes 50-90 ns per copy, which at two to four boxes a
+                // stage is longer than the stage's MMAs (256 x 256 x 64: 270 ns).
+                const int xl = !kTrain ? xn
+                               : xn <= C::kXBoxRows ? C::kXBoxRows
+                               : xn <= C::kXBoxMid  ? C::kXBoxMid
+                                                    : kMaxN / kCta;
                 // bytes landing on the (leader's) full barrier per stage: both CTAs' shares
-                const uint32_t bytes = kCta * (C::kNW * C::kWTileBytes + xn * C::kRowBytes);
+                const uint32_t bytes = kCta * (C::kNW * C::kWTileBytes + xl * C::kRowBytes);
                 const uint64_t pol_w = t.nch > 1 ? pol_w_shared : pol_w_once;
                 for (int k = it.kb; k < it.ke; ++k, ++kc) {
                     const int s = kc % C::kStages;
@@ -476,6 +492,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     if constexpr (kWMn) {
                         // boxes of 64 features by kBK rows of K; K rows past kdim read as zero
                         const int f0 = t.f0 + (int)rank * C::kFeat;
+                        if (kPair && p.w_joined)
+                            tma_load_4d_pair(st, &tm_w, fb, 0, k * C::kBK, f0 / 64, t.group, pol_w);
+                        else
 #pragma unroll
                         for (int b = 0; b < 2 * C::kNW; ++b) {
                             if (kPair)
@@ -491,14 +510,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     }
                     uint8_t* xs = st + C::kNW * C::kWTileBytes;
                     int r = 0;
-                    if (kMaxN / kCta > C::kXBoxMid && xn == kMaxN / kCta) {
+                    if (kMaxN / kCta > C::kXBoxMid && xl == kMaxN / kCta) {
                         load(xs, &tm_xbig, xrow, pol_x);
-                        r = xn;
+                        r = xl;
                     }
                     if (kMaxN / kCta >= C::kXBoxMid)
-                        for (; r + C::kXBoxMid <= xn; r += C::kXBoxMid)
+                        for (; r + C::kXBoxMid <= xl; r += C::kXBoxMid)
                             load(xs + r * C::kRowBytes, &tm_x64, xrow + r, pol_x);
-                    for (; r < xn; r += C::kXBoxRows) load(xs + r * C::kRowBytes, &tm_x, xrow + r, pol_x);
+                    for (; r < xl; r += C::kXBoxRows) load(xs + r * C::kRowBytes, &tm_x, xrow + r, pol_x);
                     ++fills[s];
                 }
             }
@@ -515,9 +534,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer
         if (lane == 0 && rank == 0) {
-            uint32_t kc = 0, ac = 0;
+            // One thread issues a stage's MMAs and its commit in the time the
+            // tensor core takes for them (a pair's 256 x 256 x 64 step: 512
+            // cycles), so the stage cursor and the descriptors are kept
+            // incrementally and one commit frees the stage in both CTAs:
+            // recomputing them and committing twice took 705 cycles a step.
+            uint32_t ac = 0, s = 0, ph = 0;
             bool ok = true;
             Item it;
+            auto desc = [](uint32_t a) { return C::kRowBytes == 128 ? umma_desc_sw128(a) : umma_desc_sw64(a); };
+            auto wdesc = [desc](uint32_t a) { return kWMn ? umma_desc_mn_sw128<64>(a) : desc(a); };
+            // K of one MMA: 32 bytes along a K-major row, 16 rows of 128 bytes in an MN-major box
+            constexpr uint32_t kWStep = kWMn ? 16 * 128 / 16 : 2;
+            const uint64_t w_base = wdesc(smem_u32(stage_base));
+            const uint64_t x_base = desc(smem_u32(stage_base + C::kNW * C::kWTileBytes));
             while (ok && sched_next(sch, it)) {
                 Tile t = decode_tile(it.tile, seg, cbase, n_groups, NF, C::kFeatTile, C::kUnit, p);
                 const int b = ac % C::kNumAcc;
@@ -530,47 +560,38 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const uint32_t d_gate = tmem_base + b * C::kAccCols;
                 const uint32_t d_up = d_gate + kMaxN;
                 const uint32_t idesc = umma_idesc(Elt<T>::kMmaFmt, 128 * kCta, t.mma_n) | (kWMn ? kIdescAMn : 0u);
-                for (int k = it.kb; k < it.ke; ++k, ++kc) {
-                    const int s = kc % C::kStages;
-                    const uint32_t ph = (kc / C::kStages) & 1u;
+                uint32_t acc = 0;
+                for (int k = it.kb; k < it.ke; ++k) {
                     if (!mbar_wait_bounded(&full[s], ph, deadline, abort_flag)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    uint8_t* st = stage_base + s * C::kStageBytes;
-                    auto desc = [](uint32_t a) { return C::kRowBytes == 128 ? umma_desc_sw128(a) : umma_desc_sw64(a); };
-                    auto wdesc = [desc](uint32_t a) { return kWMn ? umma_desc_mn_sw128<64>(a) : desc(a); };
-                    // K of one MMA: 32 bytes along a K-major row, 16 rows of 128 bytes in an MN-major box
-                    constexpr uint32_t kWStep = kWMn ? 16 * 128 / 16 : 2;
-                    const uint64_t a0 = wdesc(smem_u32(st));
-                    const uint64_t a1 = wdesc(smem_u32(st + C::kWTileBytes));
-                    const uint64_t bx = desc(smem_u32(st + C::kNW * C::kWTileBytes));
+                    const uint64_t a0 = w_base + s * (C::kStageBytes >> 4);
+                    const uint64_t a1 = a0 + (C::kWTileBytes >> 4);
+                    const uint64_t bx = x_base + s * (C::kStageBytes >> 4);
 #pragma unroll
                     for (int kk = 0; kk < C::kKSteps; ++kk) {
-                        const uint32_t acc = (k > it.kb || kk > 0) ? 1u : 0u;
+                        const uint32_t ac_kk = kk > 0 ? 1u : acc;
                         if (kPair) {
-                            umma_pair_bf16(d_gate, a0 + kWStep * kk, bx + 2 * kk, idesc, acc);
-                            if (kTwo) umma_pair_bf16(d_up, a1 + kWStep * kk, bx + 2 * kk, idesc, acc);
+                            umma_pair_bf16(d_gate, a0 + kWStep * kk, bx + 2 * kk, idesc, ac_kk);
+                            if (kTwo) umma_pair_bf16(d_up, a1 + kWStep * kk, bx + 2 * kk, idesc, ac_kk);
                         } else {
-                            umma<T>(d_gate, a0 + kWStep * kk, bx + 2 * kk, idesc, acc);
-                            if (kTwo) umma<T>(d_up, a1 + kWStep * kk, bx + 2 * kk, idesc, acc);
+                            umma<T>(d_gate, a0 + kWStep * kk, bx + 2 * kk, idesc, ac_kk);
+                            if (kTwo) umma<T>(d_up, a1 + kWStep * kk, bx + 2 * kk, idesc, ac_kk);
                         }
                     }
-                    if (kPair) {  // the stage is free in both CTAs
-                        umma_commit_pair(smem_u32(&empty[s]));
-                        umma_commit_pair(map_to_rank(smem_u32(&empty[s]), 1));
-                    } else {
-                        umma_commit(&empty[s]);
+                    acc = 1;
+                    if (kPair) umma_commit_pair_both(&empty[s]);  // the stage is free in both CTAs
+                    else umma_commit(&empty[s]);
+                    if (++s == C::kStages) {
+                        s = 0;
+                        ph ^= 1u;
                     }
                 }
                 if (!ok) break;
-                if (kPair) {
-                    umma_commit_pair(smem_u32(&tfull[b]));
-                    umma_commit_pair(map_to_rank(smem_u32(&tfull[b]), 1));
-                } else {
-                    umma_commit(&tfull[b]);
-                }
+                if (kPair) umma_commit_pair_both(&tfull[b]);
+                else umma_commit(&tfull[b]);
                 ++ac;
             }
             if (!ok) {
@@ -601,6 +622,50 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             Tile t = decode_tile(it.tile, seg, cbase, n_groups, NF, C::kFeatTile, C::kUnit, p);
             const int b = ac % C::kNumAcc;
             const uint32_t aph = (ac / C::kNumAcc) & 1u;
+            // kEpiSwiGLUGrad: the warp's pre-activations come through shared memory,
+            // two blocks of 16 tokens ahead of the one in hand (the epilogue of the
+            // first version, which loaded them from global memory where it used
+            // them, took 80 us a tile on their latency; the MMAs of a tile of
+            // K = 4096 take 18 us).
+            const int fw = t.f0 + (int)rank * C::kFeat + quad * 32;  // the warp's first feature
+            const int cend = t.nrows < cbeg + kHalfN ? t.nrows : cbeg + kHalfN;  // this half's real columns
+            const OutT* pre_in = nullptr;
+            OutT* pre_buf = nullptr;
+            if constexpr (kEpi == kEpiSwiGLUGrad) {
+                pre_in = reinterpret_cast<const OutT*>(p.pre) + (long long)t.row0 * 2 * p.n_out + fw;
+                pre_buf = reinterpret_cast<OutT*>(pre_base + (warp - 2) * (C::kPreBufs * C::kPreBlockBytes));
+            }
+            auto pre_fetch = [&](int c0) {
+                if constexpr (kEpi == kEpiSwiGLUGrad) {
+                    OutT* dst = pre_buf + ((c0 - cbeg) / 16) % C::kPreBufs * (C::kPreBlockBytes / (int)sizeof(OutT));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        // 16-byte piece q of a token's 64 bytes; rows 0..15 gate, 16..31 up
+                        const int piece = j * 32 + lane, row = piece >> 2, q = piece & 3;
+                        const int tok = c0 + (row & 15);
+                        if (tok < cend && fw + q * 8 < p.n_out)
+                            cp_async16(dst + row * 32 + q * 8, pre_in + (long long)tok * 2 * p.n_out +
+                                                                   (row >= 16 ? p.n_out : 0) + q * 8);
+                    }
+                    cp_async_commit();
+                }
+            };
+            auto pre_begin = [&]() {
+                if constexpr (kEpi == kEpiSwiGLUGrad) {
+                    __syncwarp();  // every lane is past the last tile's blocks
+                    pre_fetch(cbeg);
+                    pre_fetch(cbeg + 16);
+                }
+            };
+            // the block of c0, when it has landed; every lane is then past the block
+            // before it, whose place takes the block after next
+            auto pre_next = [&](int c0) {
+                cp_async_wait<1>();
+                __syncwarp();
+                pre_fetch(c0 + 32);
+                return pre_buf + ((c0 - cbeg) / 16) % C::kPreBufs * (C::kPreBlockBytes / (int)sizeof(OutT));
+            };
+            if (!it.split) pre_begin();  // a split tile: only the block that finishes it reads them
             // every epilogue thread goes on, or all leave (the split path below
             // meets at named barriers, which a thread that left would never reach)
             const bool got = mbar_wait_bounded(&tfull[b], aph, deadline, abort_flag);
@@ -616,7 +681,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const bool v0 = f < p.n_out;
             const bool v1 = kEpi == kEpiWide ? (f + 128 < p.n_out) : (kSwiGLU && v0);
             OutT* orow = out + (long long)t.row0 * p.out_ld + f;
-            const int cend = t.nrows < cbeg + kHalfN ? t.nrows : cbeg + kHalfN;  // this half's real columns
             // kCh columns of the first (and second) accumulator from column c0, one wait
             auto load_cols = [&](int c0, float (&g)[kCh], float (&u)[kCh]) {
                 uint32_t ga[kCh], ua[kCh];
@@ -636,8 +700,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             };
             auto release = [&]() {
                 tc_fence_before();
-                if (kPair && rank != 0) mbar_arrive_cluster(map_to_rank(smem_u32(&tempty[b]), 0));
-                else mbar_arrive(&tempty[b]);
+                __syncwarp();  // one arrival per warp
+                if (lane == 0) {
+                    if (kPair && rank != 0) mbar_arrive_cluster(map_to_rank(smem_u32(&tempty[b]), 0));
+                    else mbar_arrive(&tempty[b]);
+                }
             };
             // g: first accumulator, u: second (up projection, or features f + 128)
             const int nrows = t.nrows;
@@ -649,7 +716,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if constexpr (kEpi == kEpiSwiGLUTrain || kEpi == kEpiSwiGLUGrad)
                 prow = reinterpret_cast<OutT*>(p.pre) + (long long)t.row0 * 2 * p.n_out + f;
             const int n_out = p.n_out;
-            auto emit = [orow, prow, n_out, nrows, out_ld, v0, v1](int c0, float (&g)[16], float (&u)[16]) {
+            auto emit = [orow, prow, n_out, nrows, out_ld, v0, v1, lane, &pre_next](int c0, float (&g)[16], float (&u)[16]) {
                 const int n = nrows - c0 < 16 ? nrows - c0 : 16;
                 if constexpr (kEpi == kEpiSwiGLUTrain) {
                     if (v0) {
@@ -666,23 +733,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     return;
                 }
                 if constexpr (kEpi == kEpiSwiGLUGrad) {
+                    // this lane's feature of the block read ahead, 16 tokens of gate, then of up
+                    const OutT* pb = pre_next(c0) + lane;
                     if (v0) {
-                        float pg[16], pu[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             if (i < n) {
-                                const OutT* pr = prow + (long long)(c0 + i) * 2 * n_out;
-                                pg[i] = Elt<OutT>::to_f(pr[0]);
-                                pu[i] = Elt<OutT>::to_f(pr[n_out]);
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            if (i < n) {
-                                const float sg = __fdividef(1.f, 1.f + __expf(-pg[i]));
+                                const float pg = Elt<OutT>::to_f(pb[i * 32]), pu = Elt<OutT>::to_f(pb[(16 + i) * 32]);
+                                const float sg = __fdividef(1.f, 1.f + __expf(-pg));
                                 OutT* o = orow + (c0 + i) * out_ld;
-                                store_out<OutT>(o, g[i] * pu[i] * sg * (1.f + pg[i] * (1.f - sg)));
-                                store_out<OutT>(o + n_out, g[i] * pg[i] * sg);
+                                store_out<OutT>(o, g[i] * pu * sg * (1.f + pg * (1.f - sg)));
+                                store_out<OutT>(o + n_out, g[i] * pg * sg);
                             }
                         }
                     }
@@ -825,6 +886,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
                 if (arrived == ncontrib - 1) {
                     // last to arrive: sum every contribution in block order, then the epilogue
+                    pre_begin();
                     for (int c0 = cbeg; c0 < cend; c0 += 16) {
                         float g[16], u[16];
 #pragma unroll
@@ -895,6 +957,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             }
             ++ac;
         }
+        if constexpr (kEpi == kEpiSwiGLUGrad) cp_async_wait<0>();
     }
 
     tc_fence_before();

@@ -62,6 +62,25 @@ inline bool make_map3(CUtensorMap* m, CUtensorMapDataType dt, int elt_bytes, con
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [n, rows, cols] matrices of 16-bit elements, cols a multiple of 64, as
+// (64 columns, rows, cols / 64, n): one box takes `chunks` 64-column blocks of
+// box_rows rows, laid one after the other with the 128-byte swizzle.  (Rows
+// whose length is no multiple of 64 have no such view inside the tensor.)
+inline bool make_map_cols(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int n, long long rows, int cols,
+                          int box_rows, int chunks) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn || cols % 64) return false;
+    const cuuint64_t row = static_cast<cuuint64_t>(cols) * 2;
+    cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(cols / 64),
+                          static_cast<cuuint64_t>(n)};
+    cuuint64_t strides[3] = {row, 128, row * static_cast<cuuint64_t>(rows)};
+    cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(chunks), 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(m, dt, 4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Blocks of `kern` (a persistent kernel on clusters of kCta, one block per SM)
 // that can be resident at once on the current device, with its shared-memory
 // limit raised; cached per device in `cache` (0: not asked yet).
@@ -116,7 +135,9 @@ int launch_variant(const GemmLaunch& L, const GemmCtl& ctl, int num_sms, cudaStr
     if ((rc = resident_blocks(kern, C::kSmemBytes, kGemmThreads, kCta, d, cache, &grid_blocks)) != 0) return rc;
     CUtensorMap tm_w, tm_x, tm_x64, tm_xbig;
     constexpr int rb = C::kRowBytes;
-    if (kWMn ? !make_map3(&tm_w, Elt<T>::kTma, Elt<T>::kBytes, L.w, L.n_groups, L.kdim, L.n_out, C::kBK)
+    const bool joined = kWMn && kCta == 2 && L.n_out % 64 == 0;
+    if (joined ? !make_map_cols(&tm_w, Elt<T>::kTma, L.w, L.n_groups, L.kdim, L.n_out, C::kBK, 2 * C::kNW)
+        : kWMn ? !make_map3(&tm_w, Elt<T>::kTma, Elt<T>::kBytes, L.w, L.n_groups, L.kdim, L.n_out, C::kBK)
              : !make_map(&tm_w, Elt<T>::kTma, Elt<T>::kBytes, L.w, L.w_rows, L.kdim, 128, rb))
         return -3;
     if (!make_map(&tm_x, Elt<T>::kTma, Elt<T>::kBytes, L.x, L.x_rows, L.kdim, C::kXBoxRows, rb)) return -3;
@@ -133,6 +154,7 @@ int launch_variant(const GemmLaunch& L, const GemmCtl& ctl, int num_sms, cudaStr
     p.out = L.out;
     p.out_ld = L.out_ld;
     p.pre = L.pre;
+    p.w_joined = joined ? 1 : 0;
     p.counters = ctl.counters;
     p.partials = ctl.partials;
     p.status = ctl.status;
