@@ -167,16 +167,35 @@ def _need_cuda(*ts):
             raise ValueError("tensors must be contiguous CUDA tensors")
 
 
-def _arg(name, t, shape, dtype):
-    """One tensor argument of the training operators: on the current device,
-    contiguous, of this type and shape (None passes)."""
+def _dev():
+    # before CUDA is initialised no tensor can be on a device: any index refuses them
+    return torch.device("cuda", torch.cuda.current_device() if torch.cuda.is_initialized() else 0)
+
+
+def _arg(name, t, shape, dtype, dev=None):
+    """One tensor argument of the training operators: on the current device
+    (`dev`), contiguous, of this type and shape (None passes)."""
     if t is None:
         return
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.dtype is dtype and t.shape == shape and t.device == (dev or _dev()) and t.is_contiguous():
+        return
+    if not t.is_cuda or t.device != (dev or _dev()):
         raise ValueError(f"{name} must be on the current CUDA device")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                         f"not {t.dtype} {tuple(t.shape)}")
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, "
+                     f"not {t.dtype} {tuple(t.shape)}")
+
+
+def _a(t):
+    """A tensor's address as an integer argument (None: NULL)."""
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(dev):
+    """The handle of the current stream of `dev`."""
+    return torch.cuda.current_stream(dev).cuda_stream if _stream_of is None else _stream_of(dev.index)
+
+
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object around it
 
 
 def _act_dtype(cfg):
@@ -634,67 +653,68 @@ def tp_layer_forward(cfg_local, x, w_r, w13, w2, ws, w13_sh=None, w2_sh=None, lo
 # --------------------------------------------------------------- training
 # The gradients of the layer's steps and the norms around the block.  Buffers
 # with P_max rows are padded_rows_max(cfg) long; their rows at and past P are
-# left untouched.
-
-def _perm_arg(cfg, name, t, width, dtype=None):
-    _arg(name, t, (max(padded_rows_max(cfg), 1), width), dtype or _act_dtype(cfg))
-
+# left untouched.  The calls cost their checks, the allocation of the outputs
+# that are not given, and one ctypes call: at one token that, not the kernel,
+# is the time, so each argument is looked at once.
 
 def combine_grad(cfg, dout, y_perm, pos, w, sorted_ids, scalars, dy_perm=None, dw=None):
     """(dy_perm, dw) of the combine; dy_perm may be y_perm itself."""
-    dt = _act_dtype(cfg)
-    _arg("dout", dout, (cfg.T, cfg.H), dt)
-    _perm_arg(cfg, "y_perm", y_perm, cfg.H)
-    _arg("pos", pos, (cfg.T * cfg.K,), torch.int32)
-    _arg("w", w, (cfg.T, cfg.K), torch.float32)
-    _arg("sorted_ids", sorted_ids, (padded_rows_max(cfg),), torch.int32)
-    _arg("scalars", scalars, (4,), torch.int32)
+    dt, dev, T, K, H, Pm = _act_dtype(cfg), _dev(), cfg.T, cfg.K, cfg.H, padded_rows_max(cfg)
+    perm = (max(Pm, 1), H)
+    _arg("dout", dout, (T, H), dt, dev)
+    _arg("y_perm", y_perm, perm, dt, dev)
+    _arg("pos", pos, (T * K,), torch.int32, dev)
+    _arg("w", w, (T, K), torch.float32, dev)
+    _arg("sorted_ids", sorted_ids, (Pm,), torch.int32, dev)
+    _arg("scalars", scalars, (4,), torch.int32, dev)
     if dy_perm is None:
         dy_perm = torch.empty_like(y_perm)
+    else:
+        _arg("dy_perm", dy_perm, perm, dt, dev)
     if dw is None:
-        dw = torch.empty((cfg.T, cfg.K), dtype=torch.float32, device=dout.device)
-    _perm_arg(cfg, "dy_perm", dy_perm, cfg.H)
-    _arg("dw", dw, (cfg.T, cfg.K), torch.float32)
-    _check(lib().moe_combine_grad(ctypes.byref(cfg), _p(dout), _p(y_perm), _p(pos), _p(w), _p(sorted_ids),
-                                  _p(scalars), _p(dy_perm), _p(dw), _stream()), "moe_combine_grad")
+        dw = torch.empty_like(w)
+    else:
+        _arg("dw", dw, (T, K), torch.float32, dev)
+    _check(lib().moe_combine_grad(ctypes.byref(cfg), _a(dout), _a(y_perm), _a(pos), _a(w), _a(sorted_ids),
+                                  _a(scalars), _a(dy_perm), _a(dw), _raw_stream(dev)), "moe_combine_grad")
     return dy_perm, dw
 
 
 def permute_grad(cfg, dx_perm, pos, dx_add=None, dx=None):
     """dx [T, H] of the permute, plus dx_add."""
-    dt = _act_dtype(cfg)
-    _perm_arg(cfg, "dx_perm", dx_perm, cfg.H)
-    _arg("pos", pos, (cfg.T * cfg.K,), torch.int32)
-    _arg("dx_add", dx_add, (cfg.T, cfg.H), dt)
+    dt, dev, TH = _act_dtype(cfg), _dev(), (cfg.T, cfg.H)
+    _arg("dx_perm", dx_perm, (max(padded_rows_max(cfg), 1), cfg.H), dt, dev)
+    _arg("pos", pos, (cfg.T * cfg.K,), torch.int32, dev)
+    _arg("dx_add", dx_add, TH, dt, dev)
     if dx is None:
-        dx = torch.empty((cfg.T, cfg.H), dtype=dt, device=dx_perm.device)
-    _arg("dx", dx, (cfg.T, cfg.H), dt)
-    _check(lib().moe_permute_grad(ctypes.byref(cfg), _p(dx_perm), _p(pos), _p(dx_add), _p(dx), _stream()),
+        dx = dx_perm.new_empty(TH)
+    else:
+        _arg("dx", dx, TH, dt, dev)
+    _check(lib().moe_permute_grad(ctypes.byref(cfg), _a(dx_perm), _a(pos), _a(dx_add), _a(dx), _raw_stream(dev)),
            "moe_permute_grad")
     return dx
 
 
 def route_grad(cfg, logits, ids, dw, dlogits=None):
     """dlogits [T, E] of the top-K gate from the gate weights' gradient."""
-    _arg("logits", logits, (cfg.T, cfg.E), torch.float32)
-    _arg("ids", ids, (cfg.T, cfg.K), torch.int32)
-    _arg("dw", dw, (cfg.T, cfg.K), torch.float32)
+    dev, TE, TK = _dev(), (cfg.T, cfg.E), (cfg.T, cfg.K)
+    _arg("logits", logits, TE, torch.float32, dev)
+    _arg("ids", ids, TK, torch.int32, dev)
+    _arg("dw", dw, TK, torch.float32, dev)
     if dlogits is None:
-        dlogits = torch.empty((cfg.T, cfg.E), dtype=torch.float32, device=logits.device)
-    _arg("dlogits", dlogits, (cfg.T, cfg.E), torch.float32)
-    _check(lib().moe_route_grad(ctypes.byref(cfg), _p(logits), _p(ids), _p(dw), _p(dlogits), _stream()),
+        dlogits = torch.empty_like(logits)
+    else:
+        _arg("dlogits", dlogits, TE, torch.float32, dev)
+    _check(lib().moe_route_grad(ctypes.byref(cfg), _a(logits), _a(ids), _a(dw), _a(dlogits), _raw_stream(dev)),
            "moe_route_grad")
     return dlogits
 
 
-def _norm_args(nc, residual, w_post, gate, w_next, h, n):
-    dt, TH = _act_dtype(nc), (nc.T, nc.H)
-    _arg("residual", residual, TH, dt)
-    _arg("w_post", w_post, (nc.H,), dt)
-    _arg("w_next", w_next, (nc.H,), dt)
-    _arg("gate", gate, TH if nc.gate_mode == GATE_TOKEN else (nc.H,), dt)
-    _arg("h", h, TH, dt)
-    _arg("n", n, TH, dt)
+def _norm_args(nc, dev, dt, TH, residual, w_post, gate, w_next):
+    _arg("residual", residual, TH, dt, dev)
+    _arg("w_post", w_post, TH[1:], dt, dev)
+    _arg("w_next", w_next, TH[1:], dt, dev)
+    _arg("gate", gate, TH if nc.gate_mode == GATE_TOKEN else TH[1:], dt, dev)
 
 
 def block_norm(nc, residual=None, y=None, w_post=None, gate=None, w_next=None, h=None, n=None):
@@ -704,14 +724,19 @@ def block_norm(nc, residual=None, y=None, w_post=None, gate=None, w_next=None, h
     ref = y if y is not None else residual
     if ref is None:
         raise ValueError("block_norm needs y or residual")
-    _arg("y", y, (nc.T, nc.H), _act_dtype(nc))
-    if h is None and (y is not None or w_next is None):
+    dt, dev, TH = _act_dtype(nc), _dev(), (nc.T, nc.H)
+    _arg("y", y, TH, dt, dev)
+    _norm_args(nc, dev, dt, TH, residual, w_post, gate, w_next)
+    if h is not None:
+        _arg("h", h, TH, dt, dev)
+    elif y is not None or w_next is None:
         h = torch.empty_like(ref)
-    if n is None and w_next is not None:
+    if n is not None:
+        _arg("n", n, TH, dt, dev)
+    elif w_next is not None:
         n = torch.empty_like(ref)
-    _norm_args(nc, residual, w_post, gate, w_next, h, n)
-    _check(lib().moe_block_norm(ctypes.byref(nc), _p(y), _p(residual), _p(w_post), _p(gate), _p(w_next), _p(h), _p(n),
-                                _stream()), "moe_block_norm")
+    _check(lib().moe_block_norm(ctypes.byref(nc), _a(y), _a(residual), _a(w_post), _a(gate), _a(w_next), _a(h), _a(n),
+                                _raw_stream(dev)), "moe_block_norm")
     return h, n
 
 
@@ -719,22 +744,28 @@ def combine_norm(cfg, nc, y_perm, pos, w, shared_out=None, residual=None, w_post
                  h=None, n=None, y=None, save_y=False):
     """(h, n, y): combine and block_norm in one launch; y is the combine's
     output, kept when a buffer is given or save_y is set (None otherwise)."""
-    dt, TH = _act_dtype(cfg), (cfg.T, cfg.H)
-    _perm_arg(cfg, "y_perm", y_perm, cfg.H)
-    _arg("pos", pos, (cfg.T * cfg.K,), torch.int32)
-    _arg("w", w, (cfg.T, cfg.K), torch.float32)
-    _arg("shared_out", shared_out, TH, dt)
+    dt, dev, T, H, K = _act_dtype(cfg), _dev(), cfg.T, cfg.H, cfg.K
+    TH = (T, H)
+    _arg("y_perm", y_perm, (max(padded_rows_max(cfg), 1), H), dt, dev)
+    _arg("pos", pos, (T * K,), torch.int32, dev)
+    _arg("w", w, (T, K), torch.float32, dev)
+    _arg("shared_out", shared_out, TH, dt, dev)
+    _norm_args(nc, dev, dt, TH, residual, w_post, gate, w_next)
     if h is None:
-        h = torch.empty(TH, dtype=dt, device=y_perm.device)
-    if n is None and w_next is not None:
-        n = torch.empty(TH, dtype=dt, device=y_perm.device)
-    if y is None and save_y:
-        y = torch.empty(TH, dtype=dt, device=y_perm.device)
-    _arg("y", y, TH, dt)
-    _norm_args(nc, residual, w_post, gate, w_next, h, n)
-    _check(lib().moe_combine_norm(ctypes.byref(cfg), ctypes.byref(nc), _p(y_perm), _p(pos), _p(w), _p(shared_out),
-                                  _p(residual), _p(w_post), _p(gate), _p(w_next), _p(y), _p(h), _p(n), _stream()),
-           "moe_combine_norm")
+        h = y_perm.new_empty(TH)
+    else:
+        _arg("h", h, TH, dt, dev)
+    if n is not None:
+        _arg("n", n, TH, dt, dev)
+    elif w_next is not None:
+        n = torch.empty_like(h)
+    if y is not None:
+        _arg("y", y, TH, dt, dev)
+    elif save_y:
+        y = torch.empty_like(h)
+    _check(lib().moe_combine_norm(ctypes.byref(cfg), ctypes.byref(nc), _a(y_perm), _a(pos), _a(w), _a(shared_out),
+                                  _a(residual), _a(w_post), _a(gate), _a(w_next), _a(y), _a(h), _a(n),
+                                  _raw_stream(dev)), "moe_combine_norm")
     return h, n, y
 
 
@@ -750,100 +781,107 @@ def block_norm_grad(nc, ws, h=None, dh=None, dn=None, y=None, w_post=None, gate=
     """The gradients of block_norm / combine_norm as a dict: dw_next,
     dresidual, dgate, dw_post, dy (None where the form has none; residual
     False leaves dresidual out)."""
-    dt, TH = _act_dtype(nc), (nc.T, nc.H)
-    dev = ws.device
-    _arg("ws", ws, (ws.numel(),), torch.uint8)
-    for name, t in (("dh", dh), ("dn", dn), ("y", y)):
-        _arg(name, t, TH, dt)
-    _norm_args(nc, None, w_post, gate, w_next, h, None)
-
-    def new(cond, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=dev) if cond else None
-
-    if dresidual is None:
-        dresidual = new(residual, TH, dt)
-    if dy is None:
-        dy = new(y is not None, TH, dt)
-    _arg("dresidual", dresidual, TH, dt)
-    _arg("dy", dy, TH, dt)
-    dgate = None
-    if gate is not None:
-        dgate = new(True, TH, dt) if nc.gate_mode == GATE_TOKEN else new(True, (nc.H,), torch.float32)
-    dw_post = new(w_post is not None, (nc.H,), torch.float32)
-    dw_next = new(w_next is not None, (nc.H,), torch.float32)
-    _check(lib().moe_block_norm_grad(ctypes.byref(nc), _p(h), _p(dh), _p(dn), _p(y), _p(w_post), _p(gate),
-                                     _p(w_next), _p(dresidual), _p(dy), _p(dgate), _p(dw_post), _p(dw_next), _p(ws),
-                                     ws.numel(), _stream()), "moe_block_norm_grad")
+    dt, dev, TH = _act_dtype(nc), _dev(), (nc.T, nc.H)
+    _arg("ws", ws, (ws.numel(),), torch.uint8, dev)
+    _arg("h", h, TH, dt, dev)
+    _arg("dh", dh, TH, dt, dev)
+    _arg("dn", dn, TH, dt, dev)
+    _arg("y", y, TH, dt, dev)
+    _norm_args(nc, dev, dt, TH, None, w_post, gate, w_next)
+    ref = dh if dh is not None else dn if dn is not None else y
+    if ref is None:
+        raise ValueError("block_norm_grad needs dh or dn")
+    if dresidual is not None:
+        _arg("dresidual", dresidual, TH, dt, dev)
+    elif residual:
+        dresidual = torch.empty_like(ref)
+    if dy is not None:
+        _arg("dy", dy, TH, dt, dev)
+    elif y is not None:
+        dy = torch.empty_like(ref)
+    per_token = gate is not None and nc.gate_mode == GATE_TOKEN
+    dgate = torch.empty_like(ref) if per_token else None
+    # the sums over the tokens, as rows of one buffer
+    n = (w_post is not None) + (w_next is not None) + (gate is not None and not per_token)
+    sums = list(torch.empty((n, TH[1]), dtype=torch.float32, device=dev).unbind(0)) if n else []
+    dw_post = sums.pop() if w_post is not None else None
+    dw_next = sums.pop() if w_next is not None else None
+    if sums:
+        dgate = sums.pop()
+    _check(lib().moe_block_norm_grad(ctypes.byref(nc), _a(h), _a(dh), _a(dn), _a(y), _a(w_post), _a(gate),
+                                     _a(w_next), _a(dresidual), _a(dy), _a(dgate), _a(dw_post), _a(dw_next), _a(ws),
+                                     ws.numel(), _raw_stream(dev)), "moe_block_norm_grad")
     return dict(dw_next=dw_next, dresidual=dresidual, dgate=dgate, dw_post=dw_post, dy=dy)
 
 
-def _product_args(cfg, offsets, ws, w13=None, w2=None):
-    _arg("offsets", offsets, (cfg.E + 1,), torch.int32)
-    _arg("ws", ws, (ws.numel(),), torch.uint8)
-    _arg("w13", w13, (cfg.E, 2 * cfg.I, cfg.H), _act_dtype(cfg))
-    _arg("w2", w2, (cfg.E, cfg.H, cfg.I), _act_dtype(cfg))
-
-
-def _rows_like(cfg, t, width, out):
-    return torch.empty((max(padded_rows_max(cfg), 1), width), dtype=t.dtype, device=t.device) if out is None else out
+def _product(cfg, ws, offsets, rows, weights=None):
+    """Checks of a training product: (device, (given or new) row buffers)."""
+    dt, dev, R = _act_dtype(cfg), _dev(), max(padded_rows_max(cfg), 1)
+    _arg("offsets", offsets, (cfg.E + 1,), torch.int32, dev)
+    _arg("ws", ws, (ws.numel(),), torch.uint8, dev)
+    if weights is not None:
+        _arg(weights[0], weights[1], weights[2], dt, dev)
+    out, like = [], None
+    for name, t, width in rows:
+        if t is None:
+            t = like.new_empty((R, width))
+        else:
+            _arg(name, t, (R, width), dt, dev)
+        like = t
+        out.append(t)
+    return dev, out
 
 
 def grouped_gate_up_train(cfg, x_perm, w13, offsets, ws, h13=None, act=None):
     """(h13, act): gate/up with the pre-activations [P_max, 2I] kept."""
-    _product_args(cfg, offsets, ws, w13=w13)
-    _perm_arg(cfg, "x_perm", x_perm, cfg.H)
-    h13, act = _rows_like(cfg, x_perm, 2 * cfg.I, h13), _rows_like(cfg, x_perm, cfg.I, act)
-    _perm_arg(cfg, "h13", h13, 2 * cfg.I)
-    _perm_arg(cfg, "act", act, cfg.I)
-    _check(lib().moe_grouped_gate_up_train(ctypes.byref(cfg), _p(x_perm), _p(w13), _p(offsets), _p(h13), _p(act),
-                                           _p(ws), ws.numel(), _stream()), "moe_grouped_gate_up_train")
+    I = cfg.I
+    dev, (x_perm, h13, act) = _product(cfg, ws, offsets, (("x_perm", x_perm, cfg.H), ("h13", h13, 2 * I),
+                                                          ("act", act, I)), ("w13", w13, (cfg.E, 2 * I, cfg.H)))
+    _check(lib().moe_grouped_gate_up_train(ctypes.byref(cfg), _a(x_perm), _a(w13), _a(offsets), _a(h13), _a(act),
+                                           _a(ws), ws.numel(), _raw_stream(dev)), "moe_grouped_gate_up_train")
     return h13, act
 
 
 def grouped_down_grad(cfg, dy_perm, w2, h13, offsets, ws, dh13=None):
     """dh13: the gradient through the down projection and SwiGLU (may be h13)."""
-    _product_args(cfg, offsets, ws, w2=w2)
-    _perm_arg(cfg, "dy_perm", dy_perm, cfg.H)
-    _perm_arg(cfg, "h13", h13, 2 * cfg.I)
-    dh13 = _rows_like(cfg, dy_perm, 2 * cfg.I, dh13)
-    _perm_arg(cfg, "dh13", dh13, 2 * cfg.I)
-    _check(lib().moe_grouped_down_grad(ctypes.byref(cfg), _p(dy_perm), _p(w2), _p(h13), _p(offsets), _p(dh13), _p(ws),
-                                       ws.numel(), _stream()), "moe_grouped_down_grad")
+    I = cfg.I
+    dev, (dy_perm, h13, dh13) = _product(cfg, ws, offsets, (("dy_perm", dy_perm, cfg.H), ("h13", h13, 2 * I),
+                                                            ("dh13", dh13, 2 * I)), ("w2", w2, (cfg.E, cfg.H, I)))
+    _check(lib().moe_grouped_down_grad(ctypes.byref(cfg), _a(dy_perm), _a(w2), _a(h13), _a(offsets), _a(dh13), _a(ws),
+                                       ws.numel(), _raw_stream(dev)), "moe_grouped_down_grad")
     return dh13
 
 
 def grouped_gate_up_grad(cfg, dh13, w13, offsets, ws, dx_perm=None):
     """dx_perm: the gradient through the gate/up projections."""
-    _product_args(cfg, offsets, ws, w13=w13)
-    _perm_arg(cfg, "dh13", dh13, 2 * cfg.I)
-    dx_perm = _rows_like(cfg, dh13, cfg.H, dx_perm)
-    _perm_arg(cfg, "dx_perm", dx_perm, cfg.H)
-    _check(lib().moe_grouped_gate_up_grad(ctypes.byref(cfg), _p(dh13), _p(w13), _p(offsets), _p(dx_perm), _p(ws),
-                                          ws.numel(), _stream()), "moe_grouped_gate_up_grad")
+    I = cfg.I
+    dev, (dh13, dx_perm) = _product(cfg, ws, offsets, (("dh13", dh13, 2 * I), ("dx_perm", dx_perm, cfg.H)),
+                                    ("w13", w13, (cfg.E, 2 * I, cfg.H)))
+    _check(lib().moe_grouped_gate_up_grad(ctypes.byref(cfg), _a(dh13), _a(w13), _a(offsets), _a(dx_perm), _a(ws),
+                                          ws.numel(), _raw_stream(dev)), "moe_grouped_gate_up_grad")
     return dx_perm
+
+
+def _wgrad_out(out, like, shape, name, dev):
+    if out is None:
+        return like.new_empty(shape)
+    _arg(name, out, shape, like.dtype, dev)
+    return out
 
 
 def grouped_down_wgrad(cfg, dy_perm, act, offsets, ws, dw2=None):
     """dw2 [E, H, I] from the down projection's output gradient and its input."""
-    _product_args(cfg, offsets, ws)
-    _perm_arg(cfg, "dy_perm", dy_perm, cfg.H)
-    _perm_arg(cfg, "act", act, cfg.I)
-    if dw2 is None:
-        dw2 = torch.empty((cfg.E, cfg.H, cfg.I), dtype=act.dtype, device=act.device)
-    _arg("dw2", dw2, (cfg.E, cfg.H, cfg.I), _act_dtype(cfg))
-    _check(lib().moe_grouped_down_wgrad(ctypes.byref(cfg), _p(dy_perm), _p(act), _p(offsets), _p(dw2), _p(ws),
-                                        ws.numel(), _stream()), "moe_grouped_down_wgrad")
+    dev, _ = _product(cfg, ws, offsets, (("dy_perm", dy_perm, cfg.H), ("act", act, cfg.I)))
+    dw2 = _wgrad_out(dw2, act, (cfg.E, cfg.H, cfg.I), "dw2", dev)
+    _check(lib().moe_grouped_down_wgrad(ctypes.byref(cfg), _a(dy_perm), _a(act), _a(offsets), _a(dw2), _a(ws),
+                                        ws.numel(), _raw_stream(dev)), "moe_grouped_down_wgrad")
     return dw2
 
 
 def grouped_gate_up_wgrad(cfg, dh13, x_perm, offsets, ws, dw13=None):
     """dw13 [E, 2I, H] from the pre-activations' gradient and the permuted tokens."""
-    _product_args(cfg, offsets, ws)
-    _perm_arg(cfg, "dh13", dh13, 2 * cfg.I)
-    _perm_arg(cfg, "x_perm", x_perm, cfg.H)
-    if dw13 is None:
-        dw13 = torch.empty((cfg.E, 2 * cfg.I, cfg.H), dtype=x_perm.dtype, device=x_perm.device)
-    _arg("dw13", dw13, (cfg.E, 2 * cfg.I, cfg.H), _act_dtype(cfg))
-    _check(lib().moe_grouped_gate_up_wgrad(ctypes.byref(cfg), _p(dh13), _p(x_perm), _p(offsets), _p(dw13), _p(ws),
-                                           ws.numel(), _stream()), "moe_grouped_gate_up_wgrad")
+    dev, _ = _product(cfg, ws, offsets, (("dh13", dh13, 2 * cfg.I), ("x_perm", x_perm, cfg.H)))
+    dw13 = _wgrad_out(dw13, x_perm, (cfg.E, 2 * cfg.I, cfg.H), "dw13", dev)
+    _check(lib().moe_grouped_gate_up_wgrad(ctypes.byref(cfg), _a(dh13), _a(x_perm), _a(offsets), _a(dw13), _a(ws),
+                                           ws.numel(), _raw_stream(dev)), "moe_grouped_gate_up_wgrad")
     return dw13

@@ -45,7 +45,7 @@ static_assert((kWgPanel & (kWgPanel - 1)) == 0, "panel slots by masking");
 struct WgradParams {
     const int32_t* seg;
     int n_groups, m, n;
-    int d_joined, x_joined;  // tm_d / tm_x load 128 columns in one copy
+    int d_joined, x_joined;  // tm_d / tm_x load (and tm_out stores) 128 columns in one copy
     int run;                 // tiles along n that an expert of at most 4 chunks takes with one panel of d
     unsigned* status;
     uint64_t wait_limit_ns;
@@ -384,8 +384,13 @@ __global__ void __launch_bounds__(kWgThreads, 1)
                 fence_proxy_async_shared();
                 __syncwarp();
                 if (lane == 0 && row < p.m) {
-                    if (col < p.n) tma_store_3d(&tm_out, mine, col, row, it.g, pol_out);
-                    if (col + 64 < p.n) tma_store_3d(&tm_out, mine + kWgStoreBytes / 2, col + 64, row, it.g, pol_out);
+                    if (p.x_joined) {
+                        if (col < p.n) tma_store_4d(&tm_out, mine, 0, row, col / 64, it.g, pol_out);
+                    } else {
+                        if (col < p.n) tma_store_3d(&tm_out, mine, col, row, it.g, pol_out);
+                        if (col + 64 < p.n)
+                            tma_store_3d(&tm_out, mine + kWgStoreBytes / 2, col + 64, row, it.g, pol_out);
+                    }
                     bulk_commit();
                 }
             }
@@ -417,7 +422,8 @@ int launch_wgrad(const WgradLaunch& L, const GemmCtl& ctl, cudaStream_t stream) 
     const int dj = L.m % 64 == 0, xj = L.n % 64 == 0;
     if (!(dj ? make_map_cols(&tm_d, dt, L.d, 1, L.rows, L.m, kWgBK, 2) : make_map(&tm_d, dt, 2, L.d, L.rows, L.m, kWgBK)) ||
         !(xj ? make_map_cols(&tm_x, dt, L.x, 1, L.rows, L.n, kWgBK, 2) : make_map(&tm_x, dt, 2, L.x, L.rows, L.n, kWgBK)) ||
-        !make_map3(&tm_out, dt, 2, L.out, L.n_groups, L.m, L.n, 32))
+        !(xj ? make_map_cols(&tm_out, dt, L.out, L.n_groups, L.m, L.n, 32, 2)
+             : make_map3(&tm_out, dt, 2, L.out, L.n_groups, L.m, L.n, 32)))
         return -3;
     const long long n_tiles = (L.n + 255) / 256, tiles = (long long)((L.m + 255) / 256) * n_tiles;
     if (tiles * L.n_groups > 0x7fffffffLL - d.num_sms) return -1;
