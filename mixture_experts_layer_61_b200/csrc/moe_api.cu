@@ -661,7 +661,7 @@ size_t moe_block_norm_grad_workspace_size(const moe_norm_config_t* nc) {
     if (check_norm(nc) != MOE_OK) return 0;
     DeviceInfo d;
     if (current_device(&d) != 0) return 0;
-    return align256((size_t)norm_grad_blocks(nc->T, d.num_sms) * 2 * nc->H * sizeof(float) + 1);
+    return align256((size_t)norm_grad_blocks(nc->T, nc->H, nc->dtype, d.num_sms) * 2 * nc->H * sizeof(float) + 1);
 }
 
 int moe_block_norm_grad(const moe_norm_config_t* nc, const void* h, const void* dh, const void* dn, const void* y,
@@ -687,7 +687,7 @@ int moe_block_norm_grad(const moe_norm_config_t* nc, const void* h, const void* 
     if (!workspace) return MOE_ERR_ARG;
     DeviceInfo d;
     if ((rc = current_device(&d)) != 0) return status_of(rc);
-    if (ws_bytes < (size_t)norm_grad_blocks(nc->T, d.num_sms) * 2 * nc->H * sizeof(float)) return MOE_ERR_WORKSPACE;
+    if (ws_bytes < (size_t)norm_grad_blocks(nc->T, nc->H, nc->dtype, d.num_sms) * 2 * nc->H * sizeof(float)) return MOE_ERR_WORKSPACE;
     BlockNormGradArgs a{nc->T, nc->H, nc->dtype, nc->gate_mode, nc->eps, nc->res_scale, h, dh, dn, y, w_post, gate,
                         w_next, dresidual, dy, dgate, dw_post, dw_next, static_cast<float*>(workspace)};
     return status_of(launch_block_norm_grad(a, (cudaStream_t)stream));

@@ -251,7 +251,7 @@ struct BlockNormArgs {
 };
 int launch_block_norm(const BlockNormArgs& a, cudaStream_t stream);
 // Blocks of the gradient kernel, each leaving 2 H fp32 column sums in `partials`.
-int norm_grad_blocks(int T, int num_sms);
+int norm_grad_blocks(int T, int H, int dtype, int num_sms);
 struct BlockNormGradArgs {
     int T, H, dtype, gate_mode;
     float eps, res_scale;

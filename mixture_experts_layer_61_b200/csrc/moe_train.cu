@@ -5,6 +5,7 @@
 // gradient.  All are bound by device memory at training sizes and by latency
 // at decode sizes: each makes one pass over its rows, held in registers, with
 // fp32 sums.
+#include <atomic>
 #include <climits>
 #include <type_traits>
 
@@ -95,6 +96,9 @@ __device__ __forceinline__ float block_sum(float v, float* buf) {
 }
 
 constexpr int kRowThreads = 512;  // threads per block of the row kernels, at most
+constexpr int kNormGradThreads = 1024;
+constexpr int kNormStageBytes = 216 * 1024;  // shared memory of an SM's gradient blocks
+constexpr int kMaxCachedDevices = 64;
 
 // Vectors per thread (1, 2 or 4) and threads for rows of row_vec vectors:
 // one vector a thread while that needs at most 256 threads.
@@ -273,159 +277,326 @@ int launch_block_norm(const BlockNormArgs& a, cudaStream_t stream) {
 // six sums taken in one round give both means: one barrier per token.
 // For a channel gate both dw_post and dgate are products of one column sum,
 // A = sum_t d y rho_y (dw_post = gate A, dgate = w_post A).
-// Persistent blocks take tokens block-stride; the column sums stay in
-// registers over a block's tokens, go to the workspace as one fp32 row per
-// block and are added in block order by norm_wgrad_kernel: deterministic.
-template <typename T, int kV>
-__global__ void __launch_bounds__(kRowThreads) block_norm_grad_kernel(BlockNormGradArgs a) {
+// The kernel is bound by its instructions and their latency more than by
+// memory (a row is 57 KB at 7168 bf16 with every input).  So it is laid out
+// for 1024 threads an SM: a thread holds one vector's column sums (two in rows
+// past 16 KB), and its values pass four at a time through few registers from
+// shared memory, where cp.async has brought them two rows ahead (each thread
+// copies its own vectors: no barrier).  Arithmetic is on pairs of floats
+// (f32x2), the [H] vectors stay in shared memory, the product of w_post and a
+// channel gate as fp32.  What a call has is fixed at compile time where it
+// decides what is computed (kBlock: y; kGate: the gate's mode; kNext: w_next):
+// tested in the loops it made 990 instructions of a vector's 300.  Persistent
+// blocks take tokens block-stride; their column sums go to the workspace as
+// one fp32 row per block and are added in block order by norm_wgrad_kernel:
+// deterministic.
+
+// Two floats in a register pair, and operations on both (each rounded as the
+// scalar operation).
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 f2_make(float a, float b) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void f2_split(f2 v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_both(float a) { return f2_make(a, a); }
+__device__ __forceinline__ float f2_sum(f2 v) {
+    float a, b;
+    f2_split(v, a, b);
+    return a + b;
+}
+
+// Elements 4 q .. 4 q + 3 of a 16-byte vector.
+__device__ __forceinline__ void quad(const int4* v, int q, f2 (&f)[2], const __nv_bfloat16*) {
+    const int2 x = reinterpret_cast<const int2*>(v)[q];
+    f[0] = f2_make(__int_as_float(x.x << 16), __int_as_float(x.x & 0xffff0000));
+    f[1] = f2_make(__int_as_float(x.y << 16), __int_as_float(x.y & 0xffff0000));
+}
+__device__ __forceinline__ void quad(const int4* v, int q, f2 (&f)[2], const float*) {
+    const float4 x = reinterpret_cast<const float4*>(v)[q];
+    f[0] = f2_make(x.x, x.y);
+    f[1] = f2_make(x.z, x.w);
+}
+__device__ __forceinline__ void put_quad(int4* v, int q, const f2 (&f)[2], const __nv_bfloat16*) {
+    float x[4];
+    f2_split(f[0], x[0], x[1]);
+    f2_split(f[1], x[2], x[3]);
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    __stcs(reinterpret_cast<int2*>(v) + q,
+           make_int2(*reinterpret_cast<const int*>(&a), *reinterpret_cast<const int*>(&b)));
+}
+__device__ __forceinline__ void put_quad(int4* v, int q, const f2 (&f)[2], const float*) {
+    float x[4];
+    f2_split(f[0], x[0], x[1]);
+    f2_split(f[1], x[2], x[3]);
+    __stcs(reinterpret_cast<float4*>(v) + q, make_float4(x[0], x[1], x[2], x[3]));
+}
+
+template <typename T, int kV, bool kBlock, int kGate, bool kNext>
+struct NormGradShape {
+    // the streams of a row and their places in a stage
+    static constexpr int kDh = 0, kY = 1, kH = kY + kBlock, kDn = kH + kNext, kTokGate = kDn + kNext;
+    static constexpr int kIn = kTokGate + (kGate == 2);
+    // shared memory before the stages, in 16-byte vectors a vector of the row:
+    // fp32 coefficients w_post * channel gate, then w_next (rows past 16 KB
+    // have no room for them and read them from global memory)
+    static constexpr bool kHeld = kV == 1;
+    static constexpr int kCoef = kHeld && kBlock ? (int)(4 / sizeof(T)) : 0;
+    static constexpr int kHead = kHeld ? kCoef + kNext : 0;
+};
+
+template <typename T, int kV, bool kBlock, int kGate, bool kNext>
+__global__ void __launch_bounds__(kNormGradThreads) block_norm_grad_kernel(BlockNormGradArgs a, int stages) {
+    using S = NormGradShape<T, kV, kBlock, kGate, kNext>;
     constexpr int N = Vec16<T>::N;
+    constexpr int kQ = N / 4;
+    extern __shared__ int4 smem[];  // [kHead + stages * kIn][kV][threads]
     __shared__ float red[2][32 * 8];
     pdl_launch_dependents();
     pdl_wait();
     const int row_vec = a.H / N;
-    const int4* wpost = static_cast<const int4*>(a.w_post);
-    const int4* wnext = static_cast<const int4*>(a.w_next);
-    const int4* gate = static_cast<const int4*>(a.gate);
-    const int4 zero = make_int4(0, 0, 0, 0);
+    const int nt = blockDim.x, tid = threadIdx.x, stream = kV * nt;
+    const bool post = kBlock && a.w_post != nullptr;
     const float inv_h = 1.f / a.H;
-    float acc_next[kV][N], acc_post[kV][N];
+    const T* tag = nullptr;
+    const f2 zero2 = f2_both(0.f);
+    float4* coef = reinterpret_cast<float4*>(smem);  // quad q of vector v at [v * kQ + q]
+    int4* wnext = smem + S::kCoef * stream;
+    int4* rows = smem + S::kHead * stream;
+    const int stage_vec = S::kIn * stream;
+    auto fetch = [&](long long t, int stage) {
+        if (t < a.T) {
 #pragma unroll
-    for (int j = 0; j < kV; ++j)
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc_next[j][i] = acc_post[j][i] = 0.f;
-    auto load = [&](const void* p, long long i) { return p ? __ldcs(static_cast<const int4*>(p) + i) : zero; };
-    int4 yv[kV], hv[kV], dhv[kV], dnv[kV];
-    auto load_row = [&](long long t) {
-#pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
-            const bool in = v < row_vec;
-            const long long i = t * row_vec + v;
-            yv[j] = in ? load(a.y, i) : zero;
-            dhv[j] = in ? load(a.dh, i) : zero;
-            hv[j] = in && wnext ? load(a.h, i) : zero;
-            dnv[j] = in && wnext ? load(a.dn, i) : zero;
+            for (int j = 0; j < kV; ++j) {
+                const int v = tid + j * nt;
+                if (v < row_vec) {
+                    int4* dst = rows + stage * stage_vec + v;
+                    const long long o = t * row_vec + v;
+                    if (a.dh) cp_async16(dst + S::kDh * stream, static_cast<const int4*>(a.dh) + o);
+                    if (kBlock) cp_async16(dst + S::kY * stream, static_cast<const int4*>(a.y) + o);
+                    if (kNext) {
+                        cp_async16(dst + S::kH * stream, static_cast<const int4*>(a.h) + o);
+                        cp_async16(dst + S::kDn * stream, static_cast<const int4*>(a.dn) + o);
+                    }
+                    if (kGate == 2) cp_async16(dst + S::kTokGate * stream, static_cast<const int4*>(a.gate) + o);
+                }
+            }
+        }
+        cp_async_commit();
+    };
+    auto wait = [&]() {  // the oldest stage has landed
+        if (stages == 3) cp_async_wait<2>();
+        else if (stages == 2) cp_async_wait<1>();
+        else cp_async_wait<0>();
+    };
+    // w_post * channel gate (1 where there is none) and w_next
+    auto coef_of = [&](int v, int q, f2 (&c)[2]) {
+        c[0] = c[1] = f2_both(1.f);
+        if (post) quad(static_cast<const int4*>(a.w_post) + v, q, c, tag);
+        if (kGate == 1) {
+            f2 g[2];
+            quad(static_cast<const int4*>(a.gate) + v, q, g, tag);
+            c[0] = f2_mul(c[0], g[0]);
+            c[1] = f2_mul(c[1], g[1]);
         }
     };
-    if (blockIdx.x < a.T) load_row(blockIdx.x);
-    int phase = 0;
-    for (long long t = blockIdx.x; t < a.T; t += gridDim.x, phase ^= 1) {
-        const long long gbase = a.gate_mode == 2 ? t * row_vec : 0;
-        float s[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = 0.f;
-#pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
-            if (v < row_vec) {
-                float y[N], h[N], dh[N], dn[N], c[N], f[N];
-                up<T>(yv[j], y);
-                up<T>(hv[j], h);
-                up<T>(dhv[j], dh);
-                up<T>(dnv[j], dn);
-#pragma unroll
-                for (int i = 0; i < N; ++i) c[i] = 1.f;
-                if (wpost) up<T>(__ldg(wpost + v), c);
-                if (gate) {
-                    up<T>(__ldg(gate + gbase + v), f);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) c[i] *= f[i];
-                }
-                if (wnext) {
-                    up<T>(__ldg(wnext + v), f);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) dn[i] *= f[i];
-                }
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const float cy = c[i] * y[i];
-                    s[0] += h[i] * h[i];
-                    s[1] += dn[i] * h[i];
-                    s[2] += y[i] * y[i];
-                    s[3] += cy * dh[i];
-                    s[4] += cy * dn[i];
-                    s[5] += cy * h[i];
-                }
-            }
-        }
-        block_sum8(s, red[phase]);
-        const float rh = wnext ? rsqrtf(s[0] * inv_h + a.eps) : 0.f;
-        const float mh = s[1] * inv_h * rh * rh * rh;  // h's coefficient in d
-        const float ry = wpost ? rsqrtf(s[2] * inv_h + a.eps) : 1.f;
-        const float my = wpost ? (s[3] + rh * s[4] - mh * s[5]) * inv_h * ry * ry * ry : 0.f;
-#pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            const int v = threadIdx.x + j * blockDim.x;
-            if (v < row_vec) {
-                const long long o = t * row_vec + v;
-                float y[N], h[N], d[N], dn[N], f[N], g[N];
-                up<T>(yv[j], y);
-                up<T>(hv[j], h);
-                up<T>(dhv[j], d);
-                up<T>(dnv[j], dn);
-                if (wnext) {
-                    up<T>(__ldg(wnext + v), f);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        acc_next[j][i] += dn[i] * h[i] * rh;
-                        d[i] += rh * f[i] * dn[i] - mh * h[i];
-                    }
-                }
-                if (a.dresidual) {
-#pragma unroll
-                    for (int i = 0; i < N; ++i) f[i] = a.res_scale * d[i];
-                    static_cast<int4*>(a.dresidual)[o] = down<T>(f);
-                }
-                if (a.y) {
-#pragma unroll
-                    for (int i = 0; i < N; ++i) f[i] = g[i] = 1.f;
-                    if (wpost) up<T>(__ldg(wpost + v), f);
-                    if (gate) up<T>(__ldg(gate + gbase + v), g);
-                    if (a.gate_mode == 2) {
-                        float dg[N];
-#pragma unroll
-                        for (int i = 0; i < N; ++i) {
-                            dg[i] = d[i] * y[i] * ry * f[i];
-                            acc_post[j][i] += g[i] * d[i] * y[i] * ry;
-                        }
-                        static_cast<int4*>(a.dgate)[o] = down<T>(dg);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < N; ++i) acc_post[j][i] += d[i] * y[i] * ry;
-                    }
-#pragma unroll
-                    for (int i = 0; i < N; ++i) f[i] = ry * f[i] * g[i] * d[i] - my * y[i];
-                    static_cast<int4*>(a.dy)[o] = down<T>(f);
-                }
-            }
-        }
-        if (t + gridDim.x < a.T) load_row(t + gridDim.x);
-    }
-    // one fp32 row per block: [gridDim.x][2][H]
-    float* part = a.partials + (long long)blockIdx.x * 2 * a.H;
+    auto get_coef = [&](int v, int q, f2 (&c)[2]) {
+        if (S::kHeld) quad(reinterpret_cast<const int4*>(coef + v * kQ + q), 0, c, (const float*)nullptr);
+        else coef_of(v, q, c);
+    };
+    auto get_wnext = [&](int v, int q, f2 (&f)[2]) {
+        quad((S::kHeld ? wnext : static_cast<const int4*>(a.w_next)) + v, q, f, tag);
+    };
+    for (int s = 0; s < stages - 1; ++s) fetch((long long)blockIdx.x + (long long)s * gridDim.x, s);
+    f2 acc_next[kV][N / 2], acc_post[kV][N / 2];
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
-        const int v = threadIdx.x + j * blockDim.x;
-        if (v < row_vec) {
+        const int v = tid + j * nt;
 #pragma unroll
-            for (int i = 0; i < N; i += 4) {
-                if (wnext)
-                    *reinterpret_cast<float4*>(part + (long long)v * N + i) =
-                        make_float4(acc_next[j][i], acc_next[j][i + 1], acc_next[j][i + 2], acc_next[j][i + 3]);
-                if (a.y)
-                    *reinterpret_cast<float4*>(part + a.H + (long long)v * N + i) =
-                        make_float4(acc_post[j][i], acc_post[j][i + 1], acc_post[j][i + 2], acc_post[j][i + 3]);
+        for (int i = 0; i < N / 2; ++i) acc_next[j][i] = acc_post[j][i] = zero2;
+        if (!a.dh)  // an absent dh is a row of zeros
+            for (int s = 0; s < stages; ++s) rows[s * stage_vec + S::kDh * stream + v] = make_int4(0, 0, 0, 0);
+        if (v < row_vec) {
+            if (S::kHeld && kBlock) {
+#pragma unroll
+                for (int q = 0; q < kQ; ++q) {
+                    f2 c[2];
+                    coef_of(v, q, c);
+                    float4 x;
+                    f2_split(c[0], x.x, x.y);
+                    f2_split(c[1], x.z, x.w);
+                    coef[v * kQ + q] = x;
+                }
             }
+            if (S::kHeld && kNext) wnext[v] = __ldg(static_cast<const int4*>(a.w_next) + v);
+        }
+    }
+    int stage = 0, phase = 0;
+    for (long long t = blockIdx.x; t < a.T; t += gridDim.x, phase ^= 1) {
+        // the place of the row before this one takes the row `stages - 1` ahead
+        fetch(t + (long long)(stages - 1) * gridDim.x, stage == 0 ? stages - 1 : stage - 1);
+        wait();
+        const int4* row = rows + stage * stage_vec;
+        f2 p[6];
+#pragma unroll
+        for (int i = 0; i < 6; ++i) p[i] = zero2;
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            const int v = tid + j * nt;
+            if (v < row_vec) {
+#pragma unroll
+                for (int q = 0; q < kQ; ++q) {
+                    f2 h[2], dn[2], c[2], f[2];
+                    if (kNext) {
+                        quad(row + S::kH * stream + v, q, h, tag);
+                        quad(row + S::kDn * stream + v, q, dn, tag);
+                        get_wnext(v, q, f);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            dn[i] = f2_mul(dn[i], f[i]);
+                            p[0] = f2_fma(h[i], h[i], p[0]);
+                            p[1] = f2_fma(dn[i], h[i], p[1]);
+                        }
+                    }
+                    if (post) {
+                        quad(row + S::kY * stream + v, q, f, tag);
+                        get_coef(v, q, c);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            p[2] = f2_fma(f[i], f[i], p[2]);
+                            c[i] = f2_mul(c[i], f[i]);
+                        }
+                        if (kGate == 2) {
+                            quad(row + S::kTokGate * stream + v, q, f, tag);
+                            c[0] = f2_mul(c[0], f[0]);
+                            c[1] = f2_mul(c[1], f[1]);
+                        }
+                        quad(row + S::kDh * stream + v, q, f, tag);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            p[3] = f2_fma(c[i], f[i], p[3]);
+                            if (kNext) {
+                                p[4] = f2_fma(c[i], dn[i], p[4]);
+                                p[5] = f2_fma(c[i], h[i], p[5]);
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        float s[8];
+#pragma unroll
+        for (int i = 0; i < 6; ++i) s[i] = f2_sum(p[i]);
+        s[6] = s[7] = 0.f;
+        if (kNext || kBlock) block_sum8(s, red[phase]);
+        const float rho_h = kNext ? rsqrtf(s[0] * inv_h + a.eps) : 0.f;
+        const float mean_h = kNext ? s[1] * inv_h * rho_h * rho_h * rho_h : 0.f;  // h's coefficient in d
+        const float rho_y = post ? rsqrtf(s[2] * inv_h + a.eps) : 1.f;
+        const float mean_y =
+            post ? (s[3] + rho_h * s[4] - mean_h * s[5]) * inv_h * rho_y * rho_y * rho_y : 0.f;
+        const f2 rh = f2_both(rho_h), mh = f2_both(-mean_h), ry = f2_both(rho_y), my = f2_both(-mean_y);
+        const f2 scale = f2_both(a.res_scale);
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+            const int v = tid + j * nt;
+            if (v < row_vec) {
+                const long long o = t * row_vec + v;
+#pragma unroll
+                for (int q = 0; q < kQ; ++q) {
+                    f2 d[2], x[2], f[2], g[2];
+                    quad(row + S::kDh * stream + v, q, d, tag);
+                    if (kNext) {
+                        quad(row + S::kH * stream + v, q, x, tag);
+                        quad(row + S::kDn * stream + v, q, g, tag);
+                        get_wnext(v, q, f);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            g[i] = f2_mul(g[i], rh);
+                            acc_next[j][2 * q + i] = f2_fma(g[i], x[i], acc_next[j][2 * q + i]);
+                            d[i] = f2_fma(f[i], g[i], d[i]);
+                            d[i] = f2_fma(mh, x[i], d[i]);
+                        }
+                    }
+                    if (a.dresidual) {
+                        f[0] = f2_mul(d[0], scale);
+                        f[1] = f2_mul(d[1], scale);
+                        put_quad(static_cast<int4*>(a.dresidual) + o, q, f, tag);
+                    }
+                    if (kBlock) {
+                        quad(row + S::kY * stream + v, q, x, tag);
+                        get_coef(v, q, f);
+                        if (kGate == 2) quad(row + S::kTokGate * stream + v, q, g, tag);
+                        f2 dg[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            d[i] = f2_mul(d[i], ry);
+                            if (kGate == 2) {
+                                const f2 e = f2_mul(d[i], x[i]);  // d y rho_y
+                                dg[i] = f2_mul(e, f[i]);
+                                acc_post[j][2 * q + i] = f2_fma(g[i], e, acc_post[j][2 * q + i]);
+                                d[i] = f2_mul(d[i], g[i]);
+                            } else {
+                                acc_post[j][2 * q + i] = f2_fma(d[i], x[i], acc_post[j][2 * q + i]);
+                            }
+                            f[i] = f2_fma(my, x[i], f2_mul(f[i], d[i]));
+                        }
+                        if (kGate == 2) put_quad(static_cast<int4*>(a.dgate) + o, q, dg, tag);
+                        put_quad(static_cast<int4*>(a.dy) + o, q, f, tag);
+                    }
+                }
+            }
+        }
+        stage = stage == stages - 1 ? 0 : stage + 1;
+    }
+    cp_async_wait<0>();
+    // one fp32 row per block: [gridDim.x][2][H]
+    float* part = a.partials + (long long)blockIdx.x * 2 * a.H;
+    auto put_sums = [&](float* dst, const f2* s) {
+#pragma unroll
+        for (int i = 0; i < N / 2; i += 2) {
+            float4 x;
+            f2_split(s[i], x.x, x.y);
+            f2_split(s[i + 1], x.z, x.w);
+            *reinterpret_cast<float4*>(dst + 2 * i) = x;
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < kV; ++j) {
+        const int v = tid + j * nt;
+        if (v < row_vec) {
+            if (kNext) put_sums(part + (long long)v * N, acc_next[j]);
+            if (kBlock) put_sums(part + a.H + (long long)v * N, acc_post[j]);
         }
     }
 }
 
-// The blocks' column sums added in block order: 8 groups of rows per block,
+// The blocks' column sums added in block order: 32 groups of rows per block
+// (their loads in flight at once: 8 groups took 11 us for 148 rows of 7168),
 // then the groups in order.  blockIdx.y 0: dw_next; 1: dw_post and, for a
 // channel gate, dgate.
+constexpr int kWgradGroups = 32;
+
 template <typename T>
-__global__ void __launch_bounds__(256) norm_wgrad_kernel(BlockNormGradArgs a, int n_parts) {
-    __shared__ float4 sum[8][32];
+__global__ void __launch_bounds__(32 * kWgradGroups) norm_wgrad_kernel(BlockNormGradArgs a, int n_parts) {
+    __shared__ float4 sum[kWgradGroups][32];
     pdl_launch_dependents();
     pdl_wait();
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
@@ -434,7 +605,7 @@ __global__ void __launch_bounds__(256) norm_wgrad_kernel(BlockNormGradArgs a, in
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (c < a.H) {
         const float* p = a.partials + (post ? a.H : 0) + c;
-        const int per = (n_parts + 7) / 8;
+        const int per = (n_parts + kWgradGroups - 1) / kWgradGroups;
         const int end = min(n_parts, (grp + 1) * per);
 #pragma unroll 8
         for (int r = grp * per; r < end; ++r) {
@@ -449,7 +620,7 @@ __global__ void __launch_bounds__(256) norm_wgrad_kernel(BlockNormGradArgs a, in
     __syncthreads();
     if (grp != 0 || c >= a.H) return;
 #pragma unroll
-    for (int g = 1; g < 8; ++g) {
+    for (int g = 1; g < kWgradGroups; ++g) {
         const float4 v = sum[g][lane];
         s.x += v.x;
         s.y += v.y;
@@ -471,34 +642,89 @@ __global__ void __launch_bounds__(256) norm_wgrad_kernel(BlockNormGradArgs a, in
     }
 }
 
-int norm_grad_blocks(int T, int num_sms) { return T < num_sms ? T : num_sms; }
+namespace {
+// One vector a thread, two in rows of more than 1024 vectors.
+void norm_grad_shape(int H, int dtype, int& kv, int& threads) {
+    const int row_vec = H * (dtype == 0 ? 2 : 4) / 16;
+    kv = row_vec <= kNormGradThreads ? 1 : 2;
+    threads = (((row_vec + kv - 1) / kv) + 31) / 32 * 32;
+}
+}  // namespace
+
+// Blocks of the gradient kernel: 1024 threads per SM, so that short rows are
+// not left waiting for one another, at most 16 blocks.
+int norm_grad_blocks(int T, int H, int dtype, int num_sms) {
+    int kv, threads;
+    norm_grad_shape(H, dtype, kv, threads);
+    int per_sm = kNormGradThreads / threads;
+    if (per_sm > 16) per_sm = 16;
+    const long long most = (long long)num_sms * per_sm;
+    return T < most ? T : (int)most;
+}
+
+namespace {
+template <typename T, int kV, bool kBlock, int kGate, bool kNext>
+cudaError_t launch_norm_grad_rows(const BlockNormGradArgs& a, const DeviceInfo& d, int blocks, int threads,
+                                  cudaStream_t stream) {
+    auto kern = block_norm_grad_kernel<T, kV, kBlock, kGate, kNext>;
+    static std::atomic<bool> raised[kMaxCachedDevices];  // per instantiation: the shared-memory limit
+    if (!raised[d.device].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormStageBytes);
+        if (e != cudaSuccess) return e;
+        raised[d.device].store(true, std::memory_order_release);
+    }
+    // three rows at once, fewer where the rows are so long that they do not fit
+    // (the blocks of an SM share it)
+    using S = NormGradShape<T, kV, kBlock, kGate, kNext>;
+    const int vecs = kV * threads * 16;
+    int stages = (kNormStageBytes / (kNormGradThreads / threads) - S::kHead * vecs) / (S::kIn * vecs);
+    if (stages > 3) stages = 3;
+    if (stages < 1) return cudaErrorInvalidValue;
+    return launch_kernel(kern, dim3(blocks), dim3(threads), (S::kHead + stages * S::kIn) * vecs, stream, a,
+                         stages);
+}
+
+template <typename T, int kV>
+cudaError_t launch_norm_grad_form(const BlockNormGradArgs& a, const DeviceInfo& d, int blocks, int threads,
+                                  cudaStream_t s) {
+    if (!a.y) {
+        if (a.w_next) return launch_norm_grad_rows<T, kV, false, 0, true>(a, d, blocks, threads, s);
+        return launch_norm_grad_rows<T, kV, false, 0, false>(a, d, blocks, threads, s);
+    }
+    auto gate = [&](auto g) {
+        constexpr int kGate = decltype(g)::value;
+        if (a.w_next) return launch_norm_grad_rows<T, kV, true, kGate, true>(a, d, blocks, threads, s);
+        return launch_norm_grad_rows<T, kV, true, kGate, false>(a, d, blocks, threads, s);
+    };
+    if (a.gate_mode == 0) return gate(std::integral_constant<int, 0>());
+    if (a.gate_mode == 1) return gate(std::integral_constant<int, 1>());
+    return gate(std::integral_constant<int, 2>());
+}
+}  // namespace
 
 int launch_block_norm_grad(const BlockNormGradArgs& a, cudaStream_t stream) {
     DeviceInfo d;
     int rc = current_device(&d);
     if (rc != 0) return rc;
+    if (!row_kernels_fit(a.H, a.dtype)) return -1;
     int kv, threads;
-    row_shape(a.H * (a.dtype == 0 ? 2 : 4) / 16, kv, threads);
-    if (kv * kRowThreads * 16 < a.H * (a.dtype == 0 ? 2 : 4)) return -1;
-    const int blocks = norm_grad_blocks(a.T, d.num_sms);
+    norm_grad_shape(a.H, a.dtype, kv, threads);
+    const int blocks = norm_grad_blocks(a.T, a.H, a.dtype, d.num_sms);
     if (blocks > 0) {
-        const dim3 g(blocks), b(threads);
-        cudaError_t e;
-        auto go = [&](auto tag) -> cudaError_t {
-            using E = typename std::remove_pointer<decltype(tag)>::type;
-            if (kv == 1) return launch_kernel(block_norm_grad_kernel<E, 1>, g, b, 0, stream, a);
-            if (kv == 2) return launch_kernel(block_norm_grad_kernel<E, 2>, g, b, 0, stream, a);
-            return launch_kernel(block_norm_grad_kernel<E, 4>, g, b, 0, stream, a);
-        };
-        e = a.dtype == 0 ? go((__nv_bfloat16*)nullptr) : go((float*)nullptr);
+        using bf = __nv_bfloat16;
+        const cudaError_t e =
+            a.dtype == 0 ? (kv == 1 ? launch_norm_grad_form<bf, 1>(a, d, blocks, threads, stream)
+                                    : launch_norm_grad_form<bf, 2>(a, d, blocks, threads, stream))
+                         : (kv == 1 ? launch_norm_grad_form<float, 1>(a, d, blocks, threads, stream)
+                                    : launch_norm_grad_form<float, 2>(a, d, blocks, threads, stream));
         if ((rc = launched(e)) != 0) return rc;
     }
     const bool post = a.dw_post || (a.dgate && a.gate_mode == 1);
     if (!a.dw_next && !post) return 0;
     const dim3 g((a.H / 4 + 31) / 32, post ? 2 : 1);
     return launched(a.dtype == 0
-                        ? launch_kernel(norm_wgrad_kernel<__nv_bfloat16>, g, dim3(256), 0, stream, a, blocks)
-                        : launch_kernel(norm_wgrad_kernel<float>, g, dim3(256), 0, stream, a, blocks));
+                        ? launch_kernel(norm_wgrad_kernel<__nv_bfloat16>, g, dim3(32 * kWgradGroups), 0, stream, a, blocks)
+                        : launch_kernel(norm_wgrad_kernel<float>, g, dim3(32 * kWgradGroups), 0, stream, a, blocks));
 }
 
 // ------------------------------------------------------ combine's gradient
