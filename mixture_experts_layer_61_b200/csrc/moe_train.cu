@@ -95,21 +95,23 @@ __device__ __forceinline__ float block_sum(float v, float* buf) {
     return v;
 }
 
-constexpr int kRowThreads = 512;  // threads per block of the row kernels, at most
-constexpr int kNormGradThreads = 1024;
-constexpr int kNormStageBytes = 216 * 1024;  // shared memory of an SM's gradient blocks
-constexpr int kMaxCachedDevices = 64;
-
-// Vectors per thread (1, 2 or 4) and threads for rows of row_vec vectors:
-// one vector a thread while that needs at most 256 threads.
+// A block of the row kernels holds one row: threads, at most, and the vectors
+// of a thread (1, 2, 4 or 8).  256 threads with two or more blocks an SM keep
+// more rows in flight than one block of 512.
+constexpr int kNormThreads = 256;
 void row_shape(int row_vec, int& kv, int& threads) {
-    kv = row_vec <= 256 ? 1 : (row_vec <= 2 * kRowThreads ? 2 : 4);
+    kv = 1;
+    while (kv * kNormThreads < row_vec) kv *= 2;
     threads = (((row_vec + kv - 1) / kv) + 31) / 32 * 32;
 }
 
+constexpr int kNormGradThreads = 1024;       // of the norms' gradient, an SM
+constexpr int kNormStageBytes = 216 * 1024;  // shared memory of an SM's gradient blocks
+constexpr int kMaxCachedDevices = 64;
+
 }  // namespace
 
-bool row_kernels_fit(int H, int dtype) { return H * (dtype == 0 ? 2 : 4) / 16 <= 4 * kRowThreads; }
+bool row_kernels_fit(int H, int dtype) { return H * (dtype == 0 ? 2 : 4) <= 32 * 1024; }
 
 // ------------------------------------------------------------- block norm
 // For one token:  y = the block's output (given, or the combine's weighted sum
@@ -120,7 +122,7 @@ bool row_kernels_fit(int H, int dtype) { return H * (dtype == 0 ? 2 : 4) / 16 <=
 // One block per token, the row in registers as fp32 from the first load to
 // the last store, so every output is rounded once.
 template <typename T, int kV, int kMaxK>
-__global__ void __launch_bounds__(kRowThreads) block_norm_kernel(BlockNormArgs a) {
+__global__ void __launch_bounds__(kNormThreads, kV <= 2 && kMaxK <= 8 ? 3 : 2) block_norm_kernel(BlockNormArgs a) {
     constexpr int N = Vec16<T>::N;
     constexpr bool kCombine = kMaxK > 0;
     __shared__ float red[2][32];
@@ -243,7 +245,7 @@ int launch_block_norm(const BlockNormArgs& a, cudaStream_t stream) {
     if (a.T == 0) return 0;
     int kv, threads;
     row_shape(a.H * (a.dtype == 0 ? 2 : 4) / 16, kv, threads);
-    if (kv * kRowThreads * 16 < a.H * (a.dtype == 0 ? 2 : 4)) return -1;
+    if (kv > 8) return -1;
     const dim3 g((unsigned)a.T), b(threads);
     cudaError_t e;
     auto go = [&](auto tag, auto kvc, auto kmax) -> cudaError_t {
@@ -259,7 +261,8 @@ int launch_block_norm(const BlockNormArgs& a, cudaStream_t stream) {
     auto go_v = [&](auto tag) -> cudaError_t {
         if (kv == 1) return go_k(tag, std::integral_constant<int, 1>());
         if (kv == 2) return go_k(tag, std::integral_constant<int, 2>());
-        return go_k(tag, std::integral_constant<int, 4>());
+        if (kv == 4) return go_k(tag, std::integral_constant<int, 4>());
+        return go_k(tag, std::integral_constant<int, 8>());
     };
     e = a.dtype == 0 ? go_v((__nv_bfloat16*)nullptr) : go_v((float*)nullptr);
     return launched(e);
@@ -733,7 +736,7 @@ int launch_block_norm_grad(const BlockNormGradArgs& a, cudaStream_t stream) {
 // rows it scales and is dotted with.  The blocks past the tokens zero the
 // padding rows (the weight gradients multiply them).
 template <typename T, int kV, int kMaxK>
-__global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(CombineGradArgs a) {
+__global__ void __launch_bounds__(kNormThreads, 2) combine_grad_kernel(CombineGradArgs a) {
     constexpr int N = Vec16<T>::N;
     __shared__ float red[kMaxK][32];
     pdl_launch_dependents();
@@ -756,17 +759,17 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(CombineGradAr
         return;
     }
     const long long t = blockIdx.x;
-    float d[kV][N];
+    int4 dv[kV];  // dout's row, as it came: unpacked for each of the K rows it meets
 #pragma unroll
     for (int j = 0; j < kV; ++j) {
         const int v = threadIdx.x + j * blockDim.x;
-        int4 x = make_int4(0, 0, 0, 0);
-        if (v < row_vec) x = __ldcs(static_cast<const int4*>(a.dout) + t * row_vec + v);
-        up<T>(x, d[j]);
+        dv[j] = make_int4(0, 0, 0, 0);
+        if (v < row_vec) dv[j] = __ldcs(static_cast<const int4*>(a.dout) + t * row_vec + v);
     }
-    // kB rows requested before the first is used: dy_perm may be y_perm, so no
-    // load can move above an earlier row's store by itself
-    constexpr int kB = kMaxK < 8 / kV ? kMaxK : 8 / kV;
+    // kB rows requested before the first is used (16 vectors a thread: 115 KB an
+    // SM): dy_perm may be y_perm, so no load can move above an earlier row's
+    // store by itself
+    constexpr int kB = kMaxK < 16 / kV ? kMaxK : 16 / kV;
     float dot[kMaxK];
 #pragma unroll
     for (int k0 = 0; k0 < kMaxK; k0 += kB) {
@@ -794,14 +797,15 @@ __global__ void __launch_bounds__(kRowThreads) combine_grad_kernel(CombineGradAr
                 for (int j = 0; j < kV; ++j) {
                     const int v = threadIdx.x + j * blockDim.x;
                     if (v < row_vec) {
-                        float f[N];
+                        float f[N], d[N];
                         up<T>(yv[b][j], f);
+                        up<T>(dv[j], d);
 #pragma unroll
                         for (int i = 0; i < N; ++i) {
-                            dot[k0 + b] += d[j][i] * f[i];
-                            f[i] = w[b] * d[j][i];
+                            dot[k0 + b] += d[i] * f[i];
+                            f[i] = w[b] * d[i];
                         }
-                        dy[(long long)p[b] * row_vec + v] = down<T>(f);
+                        __stcs(dy + (long long)p[b] * row_vec + v, down<T>(f));
                     }
                 }
             }
@@ -828,7 +832,7 @@ int launch_combine_grad(const CombineGradArgs& a, cudaStream_t stream) {
     if (rc != 0) return rc;
     int kv, threads;
     row_shape(a.H * (a.dtype == 0 ? 2 : 4) / 16, kv, threads);
-    if (kv * kRowThreads * 16 < a.H * (a.dtype == 0 ? 2 : 4)) return -1;
+    if (kv > 8) return -1;
     // padding rows: a warp looks at 32 slots at a time
     const long long pad_warps = (a.P_max + 31) / 32;
     long long pad_blocks = (pad_warps + threads / 32 - 1) / (threads / 32);
@@ -847,7 +851,8 @@ int launch_combine_grad(const CombineGradArgs& a, cudaStream_t stream) {
     auto go_v = [&](auto tag) -> cudaError_t {
         if (kv == 1) return go_k(tag, std::integral_constant<int, 1>());
         if (kv == 2) return go_k(tag, std::integral_constant<int, 2>());
-        return go_k(tag, std::integral_constant<int, 4>());
+        if (kv == 4) return go_k(tag, std::integral_constant<int, 4>());
+        return go_k(tag, std::integral_constant<int, 8>());
     };
     return launched(a.dtype == 0 ? go_v((__nv_bfloat16*)nullptr) : go_v((float*)nullptr));
 }
