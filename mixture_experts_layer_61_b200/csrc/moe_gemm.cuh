@@ -614,7 +614,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         constexpr bool kBf16Out = sizeof(OutT) == 2;
         constexpr int kRegs = kBf16Out ? kHalfN / 2 : kHalfN;  // packed results of one accumulator
         constexpr bool kEarly = (kEpi == kEpiPlain || kEpi == kEpiSwiGLU) && kRegs <= 64;
-        const int cbeg = half * kHalfN;
         OutT* out = reinterpret_cast<OutT*>(p.out);
         uint32_t ac = 0;
         Item it;
@@ -622,13 +621,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             Tile t = decode_tile(it.tile, seg, cbase, n_groups, NF, C::kFeatTile, C::kUnit, p);
             const int b = ac % C::kNumAcc;
             const uint32_t aph = (ac / C::kNumAcc) & 1u;
+            // this warp's token columns: half of the accumulator's, or (training,
+            // where chunks are often short of it) half of the tile's
+            const int share = kTrain ? (t.mma_n / 2 + 15) / 16 * 16 : kHalfN;
+            const int cbeg = half * share;
             // kEpiSwiGLUGrad: the warp's pre-activations come through shared memory,
             // two blocks of 16 tokens ahead of the one in hand (the epilogue of the
             // first version, which loaded them from global memory where it used
             // them, took 80 us a tile on their latency; the MMAs of a tile of
             // K = 4096 take 18 us).
             const int fw = t.f0 + (int)rank * C::kFeat + quad * 32;  // the warp's first feature
-            const int cend = t.nrows < cbeg + kHalfN ? t.nrows : cbeg + kHalfN;  // this half's real columns
+            const int cend = t.nrows < cbeg + share ? t.nrows : cbeg + share;  // this half's real columns
             const OutT* pre_in = nullptr;
             OutT* pre_buf = nullptr;
             if constexpr (kEpi == kEpiSwiGLUGrad) {

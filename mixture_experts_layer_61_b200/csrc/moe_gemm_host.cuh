@@ -160,7 +160,11 @@ int launch_variant(const GemmLaunch& L, const GemmCtl& ctl, int num_sms, cudaStr
     p.status = ctl.status;
     p.wait_limit_ns = wait_limit_ns();
     p.withhold_first_load = take_withhold_flag();
-    p.sk_min_units = 4;
+    // fewest k-iterations of a slice; training: 16 where tiles hold many tokens,
+    // whose partial sums take longer than that to add up (8 experts of 1024 x
+    // 1024, 512 tokens, down gradient: 28 us whole, 39 us in slices of 4; with 8
+    // tokens in all, gate/up gradient: 25 us whole, 18 us in slices)
+    p.sk_min_units = (kWMn || kEpi == kEpiSwiGLUTrain) && L.x_rows > 64LL * L.n_groups ? 16 : 4;
     p.max_split = L.max_split > 0 ? L.max_split : 4;
     p.split_tail = split_tail_mode();
     int grid = grid_blocks;
