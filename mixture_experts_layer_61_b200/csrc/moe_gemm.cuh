@@ -89,7 +89,7 @@ constexpr int kEpiPlain = 0, kEpiSwiGLU = 1, kEpiWide = 2, kEpiSwiGLUTrain = 3, 
 // ([out, in] used forward: K-major), or for the gradients, which contract
 // over the weights' out axis, rows of K with the features contiguous
 // (MN-major).
-template <typename T, int kEpi, int kMaxN, int kCta = 1>
+template <typename T, int kEpi, int kMaxN, int kCta = 1, bool kTrainOrder = false>
 struct GemmCfg {
     // Operand tiles are K-major rows of kRowBytes with the swizzle of that
     // width.  128-byte rows: 64-byte rows (twice the stages in the same
@@ -110,7 +110,8 @@ struct GemmCfg {
     static constexpr int kStageBytes = kNW * kWTileBytes + kXTileBytes;
     static constexpr int kAccCols = kNW * kMaxN;
     static constexpr int kNumAcc = (512 / kAccCols) >= 2 ? 2 : 1;
-    static constexpr int kTableBytes = 2 * (kMaxGroups + 1) * 4;
+    // segment and chunk tables; training: the groups' order too
+    static constexpr int kTableBytes = 2 * (kMaxGroups + 1) * 4 + (kTrainOrder ? kMaxGroups * 2 : 0);
     static constexpr int kMiscBytes = 512;
     static constexpr int kMaxStages = 16;
     // kEpiSwiGLUGrad: each epilogue warp's pre-activations, kPreBufs blocks of
@@ -237,9 +238,23 @@ __device__ __forceinline__ void sched_init(Sched& s, const GemmParams& p, int to
     s.sk_first = true;
 }
 
+// kMixed (training): the groups come by descending tokens per tile, so a tile
+// of many tokens, bound by its MMAs, stands at the front and one of few, bound
+// by reading its weights, at the back.  The whole waves are dealt back and
+// forth, which evens out the blocks' sums, and each block takes its tiles
+// alternately from both ends, one half of the blocks starting at the front and
+// the other at the back: the MMAs of the one kind then run under the reads of
+// the other.
+template <bool kMixed>
 __device__ __forceinline__ bool sched_next(Sched& s, Item& it) {
     if (s.w < s.dp_waves) {
-        it.tile = s.w * s.G + s.cta;
+        if (kMixed) {
+            const bool front = ((s.w & 1) == 0) == (s.cta < s.G / 2);
+            const long long wave = front ? s.w / 2 : s.dp_waves - 1 - s.w / 2;
+            it.tile = wave * s.G + ((wave & 1) ? s.G - 1 - s.cta : s.cta);
+        } else {
+            it.tile = s.w * s.G + s.cta;
+        }
         it.kb = 0;
         it.ke = s.KI;
         it.split = false;
@@ -300,8 +315,10 @@ __device__ __forceinline__ int chunks_of(int rows, int max_n, int unit) {
     return (units + per - 1) / per;
 }
 
+// `order` (nullable): cbase runs over the groups in that order.
 __device__ __forceinline__ Tile decode_tile_w(long long tile, const int* seg, const int* cbase, int n_groups, int NF,
-                                              int feat, int unit, int w_group_stride) {
+                                              int feat, int unit, int w_group_stride,
+                                              const uint16_t* order = nullptr) {
     // group: largest g with cbase[g] * NF <= tile
     int lo = 0, hi = n_groups - 1;
     while (lo < hi) {
@@ -315,6 +332,8 @@ __device__ __forceinline__ Tile decode_tile_w(long long tile, const int* seg, co
     int f = (int)(local / nch);
     int j = (int)(local - (long long)f * nch);
     Tile t;
+    const int first_chunk = cbase[g];
+    if (order) g = order[g];
     int start, n, mn;
     chunk_rows(seg[g + 1] - seg[g], nch, j, unit, start, n, mn);
     t.group = g;
@@ -324,13 +343,14 @@ __device__ __forceinline__ Tile decode_tile_w(long long tile, const int* seg, co
     t.mma_n = mn;
     t.wrow = g * w_group_stride + f * feat;
     t.nch = nch;
-    t.chunk = cbase[g] + j;
+    t.chunk = first_chunk + j;
     return t;
 }
 
 __device__ __forceinline__ Tile decode_tile(long long tile, const int* seg, const int* cbase, int n_groups, int NF,
-                                            int feat, int unit, const GemmParams& p) {
-    return decode_tile_w(tile, seg, cbase, n_groups, NF, feat, unit, p.w_group_stride);
+                                            int feat, int unit, const GemmParams& p,
+                                            const uint16_t* order = nullptr) {
+    return decode_tile_w(tile, seg, cbase, n_groups, NF, feat, unit, p.w_group_stride, order);
 }
 
 template <typename OutT>
@@ -354,11 +374,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     moe_gemm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x,
                     const __grid_constant__ CUtensorMap tm_x64, const __grid_constant__ CUtensorMap tm_xbig,
                     const GemmParams p) {
-    using C = GemmCfg<T, kEpi, kMaxN, kCta>;
+    constexpr bool kTrain = kWMn || kEpi == kEpiSwiGLUTrain;
+    using C = GemmCfg<T, kEpi, kMaxN, kCta, kTrain>;
     constexpr bool kSwiGLU = kEpi == kEpiSwiGLU || kEpi == kEpiSwiGLUTrain;
     static_assert(!kWMn || (Elt<T>::kBytes == 2 && C::kBK == 64), "MN-major weights: 16-bit, 64 rows of K per box");
     constexpr bool kTwo = C::kNW == 2;
-    constexpr bool kTrain = kWMn || kEpi == kEpiSwiGLUTrain;
     constexpr bool kPair = kCta == 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -366,7 +386,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     uint8_t* pre_base = smem + C::kStages * C::kStageBytes;
     int* seg = reinterpret_cast<int*>(pre_base + C::kPreBytes);
     int* cbase = seg + (kMaxGroups + 1);
-    uint8_t* misc = reinterpret_cast<uint8_t*>(cbase + (kMaxGroups + 1));
+    uint16_t* order = kTrain ? reinterpret_cast<uint16_t*>(cbase + (kMaxGroups + 1)) : nullptr;
+    uint8_t* misc = reinterpret_cast<uint8_t*>(cbase + (kMaxGroups + 1)) + (kTrain ? kMaxGroups * 2 : 0);
     uint64_t* full = reinterpret_cast<uint64_t*>(misc);
     uint64_t* empty = full + C::kStages;
     uint64_t* tfull = empty + C::kStages;
@@ -413,11 +434,32 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     for (int g = threadIdx.x; g <= n_groups; g += blockDim.x)
         seg[g] = p.seg_offsets ? p.seg_offsets[g] : (g == 0 ? 0 : p.seg_rows);
     __syncthreads();
+    if constexpr (kTrain) {
+        // groups by descending tokens per tile, the lower index first among equals
+        auto per_tile = [&](int g) {
+            const int rows = seg[g + 1] - seg[g], n = chunks_of(rows, kMaxN, C::kUnit);
+            return n > 0 ? (rows + n - 1) / n : 0;
+        };
+        int* key = cbase;  // not in use yet
+        for (int g = threadIdx.x; g < n_groups; g += blockDim.x) key[g] = per_tile(g);
+        __syncthreads();
+        for (int g = threadIdx.x; g < n_groups; g += blockDim.x) {
+            const int mine = key[g];
+            int place = 0;
+            for (int o = 0; o < n_groups; ++o) place += key[o] > mine || (key[o] == mine && o < g);
+            order[place] = (uint16_t)g;
+        }
+        __syncthreads();
+    }
     if (warp == 0) {
         int running = 0;
         for (int base = 0; base < n_groups; base += 32) {
             int g = base + lane;
-            int n = g < n_groups ? chunks_of(seg[g + 1] - seg[g], kMaxN, C::kUnit) : 0;
+            int n = 0;
+            if (g < n_groups) {
+                const int o = kTrain ? order[g] : g;
+                n = chunks_of(seg[o + 1] - seg[o], kMaxN, C::kUnit);
+            }
             int incl = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -454,8 +496,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             bool withhold = p.withhold_first_load && blockIdx.x == 0;
             bool ok = true;
             Item it;
-            while (ok && sched_next(sch, it)) {
-                Tile t = decode_tile(it.tile, seg, cbase, n_groups, NF, C::kFeatTile, C::kUnit, p);
+            while (ok && sched_next<kTrain>(sch, it)) {
+                Tile t = decode_tile(it.tile, seg, cbase, n_groups, NF, C::kFeatTile, C::kUnit, p, order);
                 // this CTA's weight rows and token rows of the tile
                 const int wrow = t.wrow + (int)rank * C::kFeat;
                 const int xn = t.mma_n / kCta;
@@ -548,8 +590,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             constexpr uint32_t kWStep = kWMn ? 16 * 128 / 16 : 2;
             const uint64_t w_base = wdesc(smem_u32(stage_base));
             const uint64_t x_base = desc(smem_u32(stage_base + C::kNW * C::kWTileBytes));
-            while (ok && sched_next(sch, it)) {
-                Tile t = decode_tile(it.tile, seg, cbase, n_groups, NF, C::kFeatTile, C::kUnit, p);
+            while (ok && sched_next<kTrain>(sch, it)) {
+                Tile t = decode_tile(it.tile, seg, cbase, n_groups, NF, C::kFeatTile, C::kUnit, p, order);
                 const int b = ac % C::kNumAcc;
                 const uint32_t aph = (ac / C::kNumAcc) & 1u;
                 if (!mbar_wait_bounded(&tempty[b], aph ^ 1u, deadline, abort_flag)) {
@@ -617,8 +659,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         OutT* out = reinterpret_cast<OutT*>(p.out);
         uint32_t ac = 0;
         Item it;
-        while (sched_next(sch, it)) {
-            Tile t = decode_tile(it.tile, seg, cbase, n_groups, NF, C::kFeatTile, C::kUnit, p);
+        while (sched_next<kTrain>(sch, it)) {
+            Tile t = decode_tile(it.tile, seg, cbase, n_groups, NF, C::kFeatTile, C::kUnit, p, order);
             const int b = ac % C::kNumAcc;
             const uint32_t aph = (ac / C::kNumAcc) & 1u;
             // this warp's token columns: half of the accumulator's, or (training,

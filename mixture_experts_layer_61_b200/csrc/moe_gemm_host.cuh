@@ -124,7 +124,8 @@ int resident_blocks(Kern kern, int smem_bytes, int threads, int cta, const Devic
 // kWMn: the weights are [n_groups, kdim, n_out], the features contiguous
 template <typename T, typename OutT, int kEpi, int kMaxN, int kCta = 1, bool kWMn = false>
 int launch_variant(const GemmLaunch& L, const GemmCtl& ctl, int num_sms, cudaStream_t stream) {
-    using C = GemmCfg<T, kEpi, kMaxN, kCta>;
+    constexpr bool kTrain = kWMn || kEpi == kEpiSwiGLUTrain;
+    using C = GemmCfg<T, kEpi, kMaxN, kCta, kTrain>;
     auto kern = moe_gemm_kernel<T, OutT, kEpi, kMaxN, kCta, kWMn>;
     if (kCta == 2 && (num_sms & 1)) return -1;
     static std::atomic<int> cache[kMaxCachedDevices];  // per instantiation
@@ -164,7 +165,7 @@ int launch_variant(const GemmLaunch& L, const GemmCtl& ctl, int num_sms, cudaStr
     // whose partial sums take longer than that to add up (8 experts of 1024 x
     // 1024, 512 tokens, down gradient: 28 us whole, 39 us in slices of 4; with 8
     // tokens in all, gate/up gradient: 25 us whole, 18 us in slices)
-    p.sk_min_units = (kWMn || kEpi == kEpiSwiGLUTrain) && L.x_rows > 64LL * L.n_groups ? 16 : 4;
+    p.sk_min_units = kTrain && L.x_rows > 64LL * L.n_groups ? 16 : 4;
     p.max_split = L.max_split > 0 ? L.max_split : 4;
     p.split_tail = split_tail_mode();
     int grid = grid_blocks;
