@@ -17,7 +17,15 @@ int launch_gemm_train(TrainGemm kind, const GemmLaunch& L, const GemmCtl& ctl, c
     switch (kind) {
         case kTrainGateUp: return launch_variant<bf, bf, kEpiSwiGLUTrain, 256, 2>(L, ctl, d.num_sms, stream);
         case kTrainDownGrad: return launch_variant<bf, bf, kEpiSwiGLUGrad, 256, 2, true>(L, ctl, d.num_sms, stream);
-        case kTrainGateUpGrad: return launch_variant<bf, bf, kEpiWide, 256, 2, true>(L, ctl, d.num_sms, stream);
+        case kTrainGateUpGrad:
+            // 512-feature tiles read 25 % fewer operand bytes; 256-feature ones where
+            // those, cut into k-slices of at least 16 steps of 64, would not give
+            // every SM pair work (8 experts of 1024 x 1024, 512 tokens: 37 us wide,
+            // 33 us; Mixtral-shaped, 64 tokens: 268 us wide, 370 us)
+            if ((long long)L.n_groups * ((L.n_out + 511) / 512) * (L.kdim < 4096 ? (L.kdim + 1023) / 1024 : 4) <
+                d.num_sms / 2)
+                return launch_variant<bf, bf, kEpiPlain, 256, 2, true>(L, ctl, d.num_sms, stream);
+            return launch_variant<bf, bf, kEpiWide, 256, 2, true>(L, ctl, d.num_sms, stream);
     }
     return -1;
 }
