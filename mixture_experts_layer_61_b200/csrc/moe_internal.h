@@ -273,6 +273,7 @@ struct CombineGradArgs {
     const int32_t* scalars;
     void* dy_perm;
     float* dw;
+    int pad_slots;  // set by the launcher
 };
 int launch_combine_grad(const CombineGradArgs& a, cudaStream_t stream);
 int launch_route_grad(int T, int E, int K, int score_fn, int renorm, const float* logits, const int32_t* ids,

@@ -591,45 +591,49 @@ __global__ void __launch_bounds__(kNormGradThreads) block_norm_grad_kernel(Block
     }
 }
 
-// The blocks' column sums added in block order: 32 groups of rows per block
-// (their loads in flight at once: 8 groups took 11 us for 148 rows of 7168),
-// then the groups in order.  blockIdx.y 0: dw_next; 1: dw_post and, for a
-// channel gate, dgate.
-constexpr int kWgradGroups = 32;
+// The blocks' column sums added in block order: a block takes 32 columns, its
+// 128 groups of threads a run of rows each (all in flight at once), then the
+// groups are added in order, eight at a time.  blockIdx.y 0: dw_next; 1:
+// dw_post and, for a channel gate, dgate.
+constexpr int kWgradGroups = 128, kWgradCols = 32;
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kWgradGroups) norm_wgrad_kernel(BlockNormGradArgs a, int n_parts) {
-    __shared__ float4 sum[kWgradGroups][32];
+__global__ void __launch_bounds__(kWgradGroups * kWgradCols / 4) norm_wgrad_kernel(BlockNormGradArgs a, int n_parts) {
+    constexpr int kLanes = kWgradCols / 4, kFold = 8;
+    __shared__ float4 sum[kWgradGroups][kLanes];
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
-    const int c = (blockIdx.x * 32 + lane) * 4;
-    const bool post = blockIdx.y == 1;
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (c < a.H) {
-        const float* p = a.partials + (post ? a.H : 0) + c;
-        const int per = (n_parts + kWgradGroups - 1) / kWgradGroups;
-        const int end = min(n_parts, (grp + 1) * per);
-#pragma unroll 8
-        for (int r = grp * per; r < end; ++r) {
-            const float4 v = __ldcs(reinterpret_cast<const float4*>(p + (long long)r * 2 * a.H));
-            s.x += v.x;
-            s.y += v.y;
-            s.z += v.z;
-            s.w += v.w;
-        }
-    }
-    sum[grp][lane] = s;
-    __syncthreads();
-    if (grp != 0 || c >= a.H) return;
-#pragma unroll
-    for (int g = 1; g < kWgradGroups; ++g) {
-        const float4 v = sum[g][lane];
+    const int lane = threadIdx.x % kLanes, grp = threadIdx.x / kLanes;
+    const int c = blockIdx.x * kWgradCols + lane * 4;
+    const bool post = blockIdx.y == 1, in = c < a.H;
+    auto add = [](float4& s, const float4& v) {
         s.x += v.x;
         s.y += v.y;
         s.z += v.z;
         s.w += v.w;
+    };
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in) {
+        const float* p = a.partials + (post ? a.H : 0) + c;
+        const int per = (n_parts + kWgradGroups - 1) / kWgradGroups;
+        const int end = min(n_parts, (grp + 1) * per);
+#pragma unroll 8
+        for (int r = grp * per; r < end; ++r)
+            add(s, __ldcs(reinterpret_cast<const float4*>(p + (long long)r * 2 * a.H)));
     }
+    sum[grp][lane] = s;
+    __syncthreads();
+    if (grp < kWgradGroups / kFold) {
+        s = sum[grp * kFold][lane];
+#pragma unroll
+        for (int g = 1; g < kFold; ++g) add(s, sum[grp * kFold + g][lane]);
+    }
+    __syncthreads();
+    if (grp < kWgradGroups / kFold) sum[grp][lane] = s;
+    __syncthreads();
+    if (grp != 0 || !in) return;
+#pragma unroll
+    for (int g = 1; g < kWgradGroups / kFold; ++g) add(s, sum[g][lane]);
     if (!post) {
         if (a.dw_next) *reinterpret_cast<float4*>(a.dw_next + c) = s;
         return;
@@ -724,10 +728,10 @@ int launch_block_norm_grad(const BlockNormGradArgs& a, cudaStream_t stream) {
     }
     const bool post = a.dw_post || (a.dgate && a.gate_mode == 1);
     if (!a.dw_next && !post) return 0;
-    const dim3 g((a.H / 4 + 31) / 32, post ? 2 : 1);
+    const dim3 g((a.H + kWgradCols - 1) / kWgradCols, post ? 2 : 1), b(kWgradGroups * kWgradCols / 4);
     return launched(a.dtype == 0
-                        ? launch_kernel(norm_wgrad_kernel<__nv_bfloat16>, g, dim3(32 * kWgradGroups), 0, stream, a, blocks)
-                        : launch_kernel(norm_wgrad_kernel<float>, g, dim3(32 * kWgradGroups), 0, stream, a, blocks));
+                        ? launch_kernel(norm_wgrad_kernel<__nv_bfloat16>, g, b, 0, stream, a, blocks)
+                        : launch_kernel(norm_wgrad_kernel<float>, g, b, 0, stream, a, blocks));
 }
 
 // ------------------------------------------------------ combine's gradient
@@ -745,15 +749,14 @@ __global__ void __launch_bounds__(kNormThreads, 2) combine_grad_kernel(CombineGr
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     int4* dy = static_cast<int4*>(a.dy_perm);
     if (blockIdx.x >= (unsigned)a.T) {
+        // pad_slots (at most 32) slots at a time, a padding row by the whole block
         const int P = a.scalars[0];
-        const long long nwarps = (long long)(gridDim.x - a.T) * nw;
-        for (long long p0 = ((long long)(blockIdx.x - a.T) * nw + warp) * 32; p0 < P; p0 += nwarps * 32) {
-            const bool pad = p0 + lane < P && __ldg(a.sorted_ids + p0 + lane) < 0;
-            unsigned m = __ballot_sync(0xffffffffu, pad);
-            while (m) {
-                const long long p = p0 + __ffs(m) - 1;
-                m &= m - 1;
-                for (int v = lane; v < row_vec; v += 32) dy[p * row_vec + v] = make_int4(0, 0, 0, 0);
+        const long long step = (long long)(gridDim.x - a.T) * a.pad_slots;
+        for (long long p0 = (long long)(blockIdx.x - a.T) * a.pad_slots; p0 < P; p0 += step) {
+            const bool pad = lane < a.pad_slots && p0 + lane < P && __ldg(a.sorted_ids + p0 + lane) < 0;
+            for (unsigned m = __ballot_sync(0xffffffffu, pad); m; m &= m - 1) {
+                int4* row = dy + (p0 + __ffs(m) - 1) * row_vec;
+                for (int v = threadIdx.x; v < row_vec; v += blockDim.x) __stcs(row + v, make_int4(0, 0, 0, 0));
             }
         }
         return;
@@ -826,16 +829,17 @@ __global__ void __launch_bounds__(kNormThreads, 2) combine_grad_kernel(CombineGr
     }
 }
 
-int launch_combine_grad(const CombineGradArgs& a, cudaStream_t stream) {
+int launch_combine_grad(const CombineGradArgs& args, cudaStream_t stream) {
     DeviceInfo d;
     int rc = current_device(&d);
     if (rc != 0) return rc;
     int kv, threads;
-    row_shape(a.H * (a.dtype == 0 ? 2 : 4) / 16, kv, threads);
+    row_shape(args.H * (args.dtype == 0 ? 2 : 4) / 16, kv, threads);
     if (kv > 8) return -1;
-    // padding rows: a warp looks at 32 slots at a time
-    const long long pad_warps = (a.P_max + 31) / 32;
-    long long pad_blocks = (pad_warps + threads / 32 - 1) / (threads / 32);
+    // few slots a block where that spreads a few padding rows over the SMs
+    CombineGradArgs a = args;
+    a.pad_slots = a.P_max < 32LL * d.num_sms ? 4 : 32;
+    long long pad_blocks = (a.P_max + a.pad_slots - 1) / a.pad_slots;
     if (pad_blocks > 4LL * d.num_sms) pad_blocks = 4LL * d.num_sms;
     if (a.T + pad_blocks > INT_MAX) return -1;
     const dim3 g((unsigned)(a.T + pad_blocks)), b(threads);
