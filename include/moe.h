@@ -1,8 +1,9 @@
 /*
  * moe.h -- C ABI of libmoe.so: the single-GPU forward of one
- * Mixture-of-Experts FFN layer on NVIDIA B200 (sm_100a), and the dense SwiGLU
+ * Mixture-of-Experts FFN layer on NVIDIA B200 (sm_100a), the dense SwiGLU
  * FFN used as its FLOP-aligned (DenseFA) and parameter-aligned (DensePA)
- * baselines.
+ * baselines, and for training the gradients of the layer's steps and the norms
+ * around it.
  *
  * The operations follow the pages on "Demystifying the Mixture of Experts
  * Serving Tax" (MLSys 2026):
@@ -495,10 +496,16 @@ int moe_tp_reduce(int n_parts, const float* const* parts, long long count, int d
  *   backward: moe_block_norm_grad, moe_combine_grad, moe_grouped_down_grad,
  *             moe_grouped_down_wgrad, moe_grouped_gate_up_grad,
  *             moe_grouped_gate_up_wgrad, moe_permute_grad, moe_route_grad.
+ * The router's own product (dlogits . w_router into x's gradient, dlogits^T . x
+ * into w_router's) is a plain matrix product of two small matrices and is left
+ * to the caller; its share of x's gradient enters moe_permute_grad as dx_add.
  * The pages cover the forward only; these follow from its formulas.  Sums are
  * fp32 in a fixed order (results are the same from run to run) and every
  * output is rounded once.  Rows of permuted buffers at and past P are left
- * untouched. */
+ * untouched.  Two calls that may run at the same time (on two streams, or in
+ * two graphs) need a workspace each.  A gate whose forward weights are NaN
+ * (every selected logit infinite, or every selected sigmoid zero under
+ * renormalisation) has NaN gradients. */
 
 /* Gradient of the combine: with dout [T, H] the gradient of its output,
  *   dy_perm[pos(t,k)] = topk_w[t,k] * dout[t]      (padding rows p < P: zero)

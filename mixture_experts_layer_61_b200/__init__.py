@@ -1,4 +1,5 @@
-"""Python binding of libmoe.so -- the B200 (sm_100a) MoE layer forward.
+"""Python binding of libmoe.so -- the B200 (sm_100a) MoE layer forward and the
+operators of its training step.
 
 Argument marshalling only: every step of the layer runs in the library's CUDA
 kernels.  Tensors are torch CUDA tensors; the work is enqueued on the current

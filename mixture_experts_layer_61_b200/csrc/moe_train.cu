@@ -3,8 +3,8 @@
 // of the top-K gate, and the norms before and after the block (with the
 // block's gate and residual scale, fused with the combine) with their
 // gradient.  All are bound by device memory at training sizes and by latency
-// at decode sizes: each makes one pass over its rows, held in registers, with
-// fp32 sums.
+// at decode sizes: each reads its rows once, keeps its sums in fp32 and rounds
+// each output once.
 #include <atomic>
 #include <climits>
 #include <type_traits>
@@ -120,7 +120,10 @@ bool row_kernels_fit(int H, int dtype) { return H * (dtype == 0 ? 2 : 4) <= 32 *
 //   h = res_scale residual + gate z
 //   n = h rsqrt(mean h^2 + eps) w_next   (the norm before the next block)
 // One block per token, the row in registers as fp32 from the first load to
-// the last store, so every output is rounded once.
+// the last store, so every output is rounded once; the K rows' vectors are all
+// requested before the first is used.  2048 tokens of 3584 bf16, K = 8, shared
+// output, both norms: 41 us, 191 MB (0.72 of the copy bandwidth); one token
+// 2.9 us.
 template <typename T, int kV, int kMaxK>
 __global__ void __launch_bounds__(kNormThreads, kV <= 2 && kMaxK <= 8 ? 3 : 2) block_norm_kernel(BlockNormArgs a) {
     constexpr int N = Vec16<T>::N;
@@ -292,7 +295,9 @@ int launch_block_norm(const BlockNormArgs& a, cudaStream_t stream) {
 // tested in the loops it made 990 instructions of a vector's 300.  Persistent
 // blocks take tokens block-stride; their column sums go to the workspace as
 // one fp32 row per block and are added in block order by norm_wgrad_kernel:
-// deterministic.
+// deterministic.  4096 tokens of 7168 bf16 with every part: 91 us, 352 MB (0.60
+// of the copy bandwidth; issue slots 63 % used); 448 threads holding rows in
+// registers took 131 us.
 
 // Two floats in a register pair, and operations on both (each rounded as the
 // scalar operation).
@@ -738,7 +743,8 @@ int launch_block_norm_grad(const BlockNormGradArgs& a, cudaStream_t stream) {
 // dy_perm[pos(t,k)] = w(t,k) dout[t];  dw(t,k) = <dout[t], y_perm[pos(t,k)]>.
 // One block per token: dout's row is read once into registers and meets the K
 // rows it scales and is dotted with.  The blocks past the tokens zero the
-// padding rows (the weight gradients multiply them).
+// padding rows (the weight gradients multiply them).  4096 tokens of 7168
+// bf16, K = 8: 196 us, 1.0 GB (0.79 of the copy bandwidth).
 template <typename T, int kV, int kMaxK>
 __global__ void __launch_bounds__(kNormThreads, 2) combine_grad_kernel(CombineGradArgs a) {
     constexpr int N = Vec16<T>::N;
@@ -870,7 +876,8 @@ int launch_combine_grad(const CombineGradArgs& args, cudaStream_t stream) {
 //   sigmoid:               dl_i = s_i (1 - s_i) dw_i
 // 1 - s is taken as the sigmoid of -l, so it keeps its digits near s = 1.
 // The row is zeroed (or given the full softmax's share), then the selected
-// entries are written; a repeated expert's shares are added first.
+// entries are written; a repeated expert's shares are added first.  Bound by
+// latency: 2048 tokens x 256 experts, K = 8: 2.8 us, 2.3 MB.
 __global__ void __launch_bounds__(256) route_grad_kernel(int T, int E, int K, int score_fn, int renorm,
                                                          const float* __restrict__ logits,
                                                          const int32_t* __restrict__ ids,
