@@ -377,3 +377,64 @@ def test_training_step_of_the_block(score_fn, gate_mode, shared):
     for k, v in want.items():
         err = (got[k].double() - v).norm() / v.norm()
         assert err <= 20 * 2.0 ** -8, (k, err.item())
+
+
+def check_products(c):
+    """The five products of one case against 64-bit products of the same inputs."""
+    H, I, E = c.cfg.H, c.cfg.I, c.cfg.E
+    t = product_tensors(c)
+    dh = c.rows(2 * I, 0.1)
+    h13, act = moe.grouped_gate_up_train(c.cfg, t["x"], t["w13"], c.off, c.ws, h13=t["h13"], act=t["act"])
+    dx = moe.grouped_gate_up_grad(c.cfg, dh, t["w13"], c.off, c.ws, dx_perm=t["dx"])
+    dh2 = moe.grouped_down_grad(c.cfg, t["dy"], t["w2"], h13, c.off, c.ws, dh13=t["dh"])
+    c.done(h13, act, dx, dh2)
+    for out, a, w in ((h13, t["x"], t["w13"].transpose(1, 2)), (dx, dh, t["w13"])):
+        v, m = c.each(lambda e, s: dot(a[s], w[e]), out.shape[1])
+        acc = R.product_bound(w.shape[1], m)
+        R.close(out[:c.P], v, HALF * (v.abs() + acc) + acc)
+    v, m = c.each(lambda e, s: dot(t["dy"][s], t["w2"][e]), I)
+    acc = R.product_bound(H, m)
+    g, u = R.f64(h13[:c.P, :I]), R.f64(h13[:c.P, I:])
+    ref = v * R.silu(g)
+    e = R.silu(g).abs() * (acc + (v.abs() + acc) * 2.0 ** -20 * (1 + g.abs()))
+    R.close(dh2[:c.P, I:], ref, HALF * (ref.abs() + e) + e, "du")
+    for out, d, r in ((moe.grouped_down_wgrad(c.cfg, t["dy"], act, c.off, c.ws), t["dy"], act),
+                      (moe.grouped_gate_up_wgrad(c.cfg, dh, t["x"], c.off, c.ws), dh, t["x"])):
+        for e in range(E):
+            a, b = c.seg[e], c.seg[e + 1]
+            v, m = dot(d[a:b].t(), r[a:b])
+            acc = R.product_bound(b - a, m.cpu())
+            R.close(out[e], v.cpu(), HALF * (v.cpu().abs() + acc) + acc, f"expert {e}")
+    moe.check_status(c.ws)
+
+
+def uneven(T, E, K, seed):
+    """Ids whose experts differ a hundredfold in tokens; some have none."""
+    g = gen(seed)
+    pref = -2.5 * torch.log(torch.arange(1, E + 1, device="cuda", dtype=torch.float32))
+    pref = pref[torch.randperm(E, generator=g, device="cuda")]
+    return torch.topk(torch.randn((T, E), generator=g, device="cuda") + pref, K, dim=1).indices.int()
+
+
+@pytest.mark.parametrize("T,H,E,K,I", [(1500, 1024, 40, 2, 264), (900, 520, 64, 4, 192), (2500, 640, 9, 3, 384)])
+def test_uneven_experts(T, H, E, K, I):
+    """Many and few rows side by side: streaming and resident weight-gradient units, mixed tile order."""
+    check_products(Case(T, H, E, K, I, ids=uneven(T, E, K, T)))
+
+
+def test_the_most_experts():
+    check_products(Case(100, 64, 1024, 8, 72, seed=3))
+
+
+@pytest.mark.parametrize("setting", ["contiguous split tail", "plain stream order"])
+def test_schedules(setting):
+    L = moe.lib()
+    try:
+        if setting == "contiguous split tail":
+            assert L.moe_set_split_tail(0) == 0
+        else:
+            L.moe_set_programmatic_launch(0)
+        check_products(Case(500, 1024, 6, 2, 520, seed=4))
+    finally:
+        L.moe_set_split_tail(1)
+        L.moe_set_programmatic_launch(1)

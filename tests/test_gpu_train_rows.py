@@ -331,3 +331,37 @@ def test_side_stream_and_graph_replay():
         want = step()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_permute_grad_of_rows_past_the_row_kernels():
+    """The permute's gradient has no limit on the row's length."""
+    T, H = 9, 40000
+    cfg, _, ids, w, al = routing(T, 5, 3, 2, H=H)
+    dx_perm = randn(moe.padded_rows_max(cfg), H, g=gen(3), dtype=torch.bfloat16)
+    dx = moe.permute_grad(cfg, dx_perm, al["pos"])
+    ref, mag = R.combine(R.f64(dx_perm), al["pos"].cpu(), torch.ones((T, 3), dtype=torch.float64))
+    R.close(dx, ref, R.rounded(ref, torch.bfloat16, mag), "dx")
+
+
+def test_two_norm_gradients_at_once():
+    """Two streams, a workspace each: the same bits as one after the other."""
+    cases = []
+    for T, H, seed in ((700, 1024, 1), (300, 4096, 2)):
+        wp, gate, wn, y = norm_inputs(T, H, torch.bfloat16, True, 1, True, seed)
+        g = gen(seed + 10)
+        h, dh, dn = (randn(T, H, g=g, dtype=torch.bfloat16) for _ in range(3))
+        nc = moe.norm_config(T, H, gate_mode=1)
+        ws = moe.alloc_workspace(moe.block_norm_grad_workspace_size(nc))
+        cases.append(lambda nc=nc, ws=ws, h=h, dh=dh, dn=dn, y=y, wp=wp, gate=gate, wn=wn: moe.block_norm_grad(
+            nc, ws, h=h, dh=dh, dn=dn, y=y, w_post=wp, gate=gate, w_next=wn))
+    want = [{k: v.clone() for k, v in f().items()} for f in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        got = []
+        for f, s in zip(cases, streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append(f())
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(a[k], b[k]) for k in b)
