@@ -73,6 +73,7 @@ struct GemmParams {
     int max_split;        // stream-K: most blocks contributing to one tile
     int split_tail;       // 1: whole waves data-parallel, the last partial wave in aligned k-slices
     int w_joined;         // MN-major weights: tm_w loads a stage's weight tiles in one copy
+    int x_joined;         // stages of several k-chunks: the tm_x maps load all of them in one copy
     void* pre;            // training epilogues: pre-activations [rows, 2 n_out], gate then up columns
 };
 
@@ -107,22 +108,23 @@ struct GemmCfg {
     static constexpr int kXBoxRows = 16;       // token rows per TMA box: 16, 64 and kMaxN
     static constexpr int kXBoxMid = 64;
     static constexpr int kXTileBytes = (kMaxN / kCta) * kRowBytes;  // this CTA's share of the token tile
-    static constexpr int kStageBytes = kNW * kWTileBytes + kXTileBytes;
+    // k-chunks of kBK a stage holds, loaded in one copy per operand: two where a
+    // chunk's MMAs (256 x 256 x 64 on a pair: 270 ns) take no longer than its two
+    // copies' issue (65 ns each and 0.7 ns a 128-byte row)
+    static constexpr int kChunks = kEpi == kEpiSwiGLUGrad ? 2 : 1;
+    static constexpr int kStageK = kBK * kChunks;
+    static constexpr int kWBytes = kNW * kWTileBytes * kChunks;  // a stage's weight tiles
+    static constexpr int kStageBytes = kWBytes + kXTileBytes * kChunks;
     static constexpr int kAccCols = kNW * kMaxN;
     static constexpr int kNumAcc = (512 / kAccCols) >= 2 ? 2 : 1;
     // segment and chunk tables; training: the groups' order too
     static constexpr int kTableBytes = 2 * (kMaxGroups + 1) * 4 + (kTrainOrder ? kMaxGroups * 2 : 0);
     static constexpr int kMiscBytes = 512;
     static constexpr int kMaxStages = 16;
-    // kEpiSwiGLUGrad: each epilogue warp's pre-activations, kPreBufs blocks of
-    // (gate, up) x 16 tokens x 32 features, read ahead of the block in hand
-    static constexpr int kPreBufs = 3;
-    static constexpr int kPreBlockBytes = 2 * 16 * 32 * Elt<T>::kBytes;
-    static constexpr int kPreBytes = kEpi == kEpiSwiGLUGrad ? kGemmEpiWarps * kPreBufs * kPreBlockBytes : 0;
-    static constexpr int kBudget = 227 * 1024 - 1024 - kTableBytes - kMiscBytes - kPreBytes;
+    static constexpr int kBudget = 227 * 1024 - 1024 - kTableBytes - kMiscBytes;
     static constexpr int kStagesRaw = kBudget / kStageBytes;
     static constexpr int kStages = kStagesRaw > kMaxStages ? kMaxStages : kStagesRaw;
-    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kPreBytes + kTableBytes + kMiscBytes;
+    static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kTableBytes + kMiscBytes;
     static_assert(kStages >= 2, "pipeline needs two stages");
     static_assert(kMaxN % kUnit == 0 && kMaxN >= kUnit && kMaxN <= 256, "MMA N range");
     static_assert(kCta == 1 || kCta == 2, "one CTA or a CTA pair");
@@ -377,14 +379,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     constexpr bool kTrain = kWMn || kEpi == kEpiSwiGLUTrain;
     using C = GemmCfg<T, kEpi, kMaxN, kCta, kTrain>;
     constexpr bool kSwiGLU = kEpi == kEpiSwiGLU || kEpi == kEpiSwiGLUTrain;
-    static_assert(!kWMn || (Elt<T>::kBytes == 2 && C::kBK == 64), "MN-major weights: 16-bit, 64 rows of K per box");
+    static_assert(!kWMn || (Elt<T>::kBytes == 2 && C::kBK == 64), "MN-major weights: 16-bit, 64 features per box row");
+    static_assert(C::kChunks == 1 || (kWMn && kCta == 2), "stages of several chunks: MN-major weights on pairs");
     constexpr bool kTwo = C::kNW == 2;
     constexpr bool kPair = kCta == 2;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* stage_base = smem;
-    uint8_t* pre_base = smem + C::kStages * C::kStageBytes;
-    int* seg = reinterpret_cast<int*>(pre_base + C::kPreBytes);
+    int* seg = reinterpret_cast<int*>(smem + C::kStages * C::kStageBytes);
     int* cbase = seg + (kMaxGroups + 1);
     uint16_t* order = kTrain ? reinterpret_cast<uint16_t*>(cbase + (kMaxGroups + 1)) : nullptr;
     uint8_t* misc = reinterpret_cast<uint8_t*>(cbase + (kMaxGroups + 1)) + (kTrain ? kMaxGroups * 2 : 0);
@@ -477,10 +479,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const uint32_t tmem_base = *tmem_holder;
 
     const int NF = (p.n_out + C::kFeatTile - 1) / C::kFeatTile;
-    const int KI = (p.kdim + C::kBK - 1) / C::kBK;
+    const int KI = (p.kdim + C::kStageK - 1) / C::kStageK;
     Sched sch;
     sched_init(sch, p, cbase[n_groups], NF, KI, kCta);
 
+    // training: rows of the box that holds a CTA's xn token rows
+    auto x_box = [](int xn) {
+        return xn <= C::kXBoxRows ? C::kXBoxRows : xn <= C::kXBoxMid ? C::kXBoxMid : kMaxN / kCta;
+    };
     if (warp == 0) {
         // ---------------------------------------------------- TMA producer
         if (lane == 0) {
@@ -506,12 +512,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 // three that holds them (rows past the chunk are not multiplied): the
                 // issuing thread takes 50-90 ns per copy, which at two to four boxes a
                 // stage is longer than the stage's MMAs (256 x 256 x 64: 270 ns).
-                const int xl = !kTrain ? xn
-                               : xn <= C::kXBoxRows ? C::kXBoxRows
-                               : xn <= C::kXBoxMid  ? C::kXBoxMid
-                                                    : kMaxN / kCta;
+                const int xl = kTrain ? x_box(xn) : xn;
                 // bytes landing on the (leader's) full barrier per stage: both CTAs' shares
-                const uint32_t bytes = kCta * (C::kNW * C::kWTileBytes + xl * C::kRowBytes);
+                const uint32_t bytes = kCta * (C::kWBytes + C::kChunks * xl * C::kRowBytes);
                 const uint64_t pol_w = t.nch > 1 ? pol_w_shared : pol_w_once;
                 for (int k = it.kb; k < it.ke; ++k, ++kc) {
                     const int s = kc % C::kStages;
@@ -535,22 +538,32 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         // boxes of 64 features by kBK rows of K; K rows past kdim read as zero
                         const int f0 = t.f0 + (int)rank * C::kFeat;
                         if (kPair && p.w_joined)
-                            tma_load_4d_pair(st, &tm_w, fb, 0, k * C::kBK, f0 / 64, t.group, pol_w);
+                            tma_load_4d_pair(st, &tm_w, fb, 0, k * C::kStageK, f0 / 64, t.group, pol_w);
                         else
 #pragma unroll
                         for (int b = 0; b < 2 * C::kNW; ++b) {
+                            uint8_t* dst = st + b * (C::kStageK * 128);
                             if (kPair)
-                                tma_load_3d_pair(st + b * (C::kWTileBytes / 2), &tm_w, fb, f0 + 64 * b, k * C::kBK, t.group,
-                                                 pol_w);
+                                tma_load_3d_pair(dst, &tm_w, fb, f0 + 64 * b, k * C::kStageK, t.group, pol_w);
                             else
-                                tma_load_3d(st + b * (C::kWTileBytes / 2), &tm_w, &full[s], f0 + 64 * b, k * C::kBK,
-                                            t.group, pol_w);
+                                tma_load_3d(dst, &tm_w, &full[s], f0 + 64 * b, k * C::kStageK, t.group, pol_w);
                         }
                     } else {
                         load(st, &tm_w, wrow, pol_w);
                         if (kTwo) load(st + C::kWTileBytes, &tm_w, wrow + (kSwiGLU ? p.up_offset : 128), pol_w);
                     }
-                    uint8_t* xs = st + C::kNW * C::kWTileBytes;
+                    uint8_t* xs = st + C::kWBytes;
+                    if constexpr (C::kChunks > 1) {
+                        const CUtensorMap* m = xl == C::kXBoxRows ? &tm_x : xl == C::kXBoxMid ? &tm_x64 : &tm_xbig;
+                        if (p.x_joined)
+                            tma_load_4d_pair(xs, m, fb, 0, xrow, k * C::kChunks, 0, pol_x);
+                        else
+                            for (int c = 0; c < C::kChunks; ++c)
+                                tma_load_2d_pair(xs + c * xl * C::kRowBytes, m, fb, k * C::kStageK + c * C::kBK, xrow,
+                                                 pol_x);
+                        ++fills[s];
+                        continue;
+                    }
                     int r = 0;
                     if (kMaxN / kCta > C::kXBoxMid && xl == kMaxN / kCta) {
                         load(xs, &tm_xbig, xrow, pol_x);
@@ -585,11 +598,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             bool ok = true;
             Item it;
             auto desc = [](uint32_t a) { return C::kRowBytes == 128 ? umma_desc_sw128(a) : umma_desc_sw64(a); };
-            auto wdesc = [desc](uint32_t a) { return kWMn ? umma_desc_mn_sw128<64>(a) : desc(a); };
+            auto wdesc = [desc](uint32_t a) { return kWMn ? umma_desc_mn_sw128<C::kStageK>(a) : desc(a); };
             // K of one MMA: 32 bytes along a K-major row, 16 rows of 128 bytes in an MN-major box
             constexpr uint32_t kWStep = kWMn ? 16 * 128 / 16 : 2;
             const uint64_t w_base = wdesc(smem_u32(stage_base));
-            const uint64_t x_base = desc(smem_u32(stage_base + C::kNW * C::kWTileBytes));
+            const uint64_t x_base = desc(smem_u32(stage_base + C::kWBytes));
             while (ok && sched_next<kTrain>(sch, it)) {
                 Tile t = decode_tile(it.tile, seg, cbase, n_groups, NF, C::kFeatTile, C::kUnit, p, order);
                 const int b = ac % C::kNumAcc;
@@ -603,6 +616,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 const uint32_t d_up = d_gate + kMaxN;
                 const uint32_t idesc = umma_idesc(Elt<T>::kMmaFmt, 128 * kCta, t.mma_n) | (kWMn ? kIdescAMn : 0u);
                 uint32_t acc = 0;
+                // from one k-chunk of the token rows to the next
+                const uint32_t x_chunk = C::kChunks > 1 ? (uint32_t)(x_box(t.mma_n / kCta) * C::kRowBytes) >> 4 : 0u;
                 for (int k = it.kb; k < it.ke; ++k) {
                     if (!mbar_wait_bounded(&full[s], ph, deadline, abort_flag)) {
                         ok = false;
@@ -613,14 +628,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     const uint64_t a1 = a0 + (C::kWTileBytes >> 4);
                     const uint64_t bx = x_base + s * (C::kStageBytes >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < C::kKSteps; ++kk) {
+                    for (int kk = 0; kk < C::kKSteps * C::kChunks; ++kk) {
                         const uint32_t ac_kk = kk > 0 ? 1u : acc;
+                        const uint64_t b = bx + (kk / C::kKSteps) * x_chunk + 2 * (kk % C::kKSteps);
                         if (kPair) {
-                            umma_pair_bf16(d_gate, a0 + kWStep * kk, bx + 2 * kk, idesc, ac_kk);
-                            if (kTwo) umma_pair_bf16(d_up, a1 + kWStep * kk, bx + 2 * kk, idesc, ac_kk);
+                            umma_pair_bf16(d_gate, a0 + kWStep * kk, b, idesc, ac_kk);
+                            if (kTwo) umma_pair_bf16(d_up, a1 + kWStep * kk, b, idesc, ac_kk);
                         } else {
-                            umma<T>(d_gate, a0 + kWStep * kk, bx + 2 * kk, idesc, ac_kk);
-                            if (kTwo) umma<T>(d_up, a1 + kWStep * kk, bx + 2 * kk, idesc, ac_kk);
+                            umma<T>(d_gate, a0 + kWStep * kk, b, idesc, ac_kk);
+                            if (kTwo) umma<T>(d_up, a1 + kWStep * kk, b, idesc, ac_kk);
                         }
                     }
                     acc = 1;
@@ -652,7 +668,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int e = (warp - 2) * 32 + lane;     // epilogue thread 0 .. 255
         constexpr int kEpiThreads = 32 * kGemmEpiWarps;
         constexpr int kHalfN = kMaxN / (kGemmEpiWarps / 4);  // token columns per warp
-        constexpr int kCh = kHalfN >= 32 ? 32 : 16;
+        constexpr int kCh = kHalfN >= 32 && kEpi != kEpiSwiGLUGrad ? 32 : 16;
         constexpr bool kBf16Out = sizeof(OutT) == 2;
         constexpr int kRegs = kBf16Out ? kHalfN / 2 : kHalfN;  // packed results of one accumulator
         constexpr bool kEarly = (kEpi == kEpiPlain || kEpi == kEpiSwiGLU) && kRegs <= 64;
@@ -667,50 +683,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             // where chunks are often short of it) half of the tile's
             const int share = kTrain ? (t.mma_n / 2 + 15) / 16 * 16 : kHalfN;
             const int cbeg = half * share;
-            // kEpiSwiGLUGrad: the warp's pre-activations come through shared memory,
-            // two blocks of 16 tokens ahead of the one in hand (the epilogue of the
-            // first version, which loaded them from global memory where it used
-            // them, took 80 us a tile on their latency; the MMAs of a tile of
-            // K = 4096 take 18 us).
-            const int fw = t.f0 + (int)rank * C::kFeat + quad * 32;  // the warp's first feature
             const int cend = t.nrows < cbeg + share ? t.nrows : cbeg + share;  // this half's real columns
-            const OutT* pre_in = nullptr;
-            OutT* pre_buf = nullptr;
+            // kEpiSwiGLUGrad: this lane's feature of 16 tokens' pre-activations, gate
+            // and up, requested one block ahead of their use (a tile's first before
+            // its MMAs are waited for); loaded where they were used, they held a tile
+            // up for 80 us, where its MMAs at K = 4096 take 18 us
+            uint16_t pre[kEpi == kEpiSwiGLUGrad ? 32 : 1];
+            const uint16_t* pre_in = nullptr;
             if constexpr (kEpi == kEpiSwiGLUGrad) {
-                pre_in = reinterpret_cast<const OutT*>(p.pre) + (long long)t.row0 * 2 * p.n_out + fw;
-                pre_buf = reinterpret_cast<OutT*>(pre_base + (warp - 2) * (C::kPreBufs * C::kPreBlockBytes));
+                const int pf = t.f0 + (int)rank * C::kFeat + r;
+                if (pf < p.n_out) pre_in = reinterpret_cast<const uint16_t*>(p.pre) + (long long)t.row0 * 2 * p.n_out + pf;
             }
             auto pre_fetch = [&](int c0) {
                 if constexpr (kEpi == kEpiSwiGLUGrad) {
-                    OutT* dst = pre_buf + ((c0 - cbeg) / 16) % C::kPreBufs * (C::kPreBlockBytes / (int)sizeof(OutT));
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        // 16-byte piece q of a token's 64 bytes; rows 0..15 gate, 16..31 up
-                        const int piece = j * 32 + lane, row = piece >> 2, q = piece & 3;
-                        const int tok = c0 + (row & 15);
-                        if (tok < cend && fw + q * 8 < p.n_out)
-                            cp_async16(dst + row * 32 + q * 8, pre_in + (long long)tok * 2 * p.n_out +
-                                                                   (row >= 16 ? p.n_out : 0) + q * 8);
+                    for (int i = 0; i < 16; ++i) {
+                        if (pre_in && c0 + i < cend) {
+                            const uint16_t* q = pre_in + (long long)(c0 + i) * 2 * p.n_out;
+                            pre[i] = q[0];
+                            pre[16 + i] = q[p.n_out];
+                        }
                     }
-                    cp_async_commit();
                 }
             };
-            auto pre_begin = [&]() {
-                if constexpr (kEpi == kEpiSwiGLUGrad) {
-                    __syncwarp();  // every lane is past the last tile's blocks
-                    pre_fetch(cbeg);
-                    pre_fetch(cbeg + 16);
-                }
-            };
-            // the block of c0, when it has landed; every lane is then past the block
-            // before it, whose place takes the block after next
-            auto pre_next = [&](int c0) {
-                cp_async_wait<1>();
-                __syncwarp();
-                pre_fetch(c0 + 32);
-                return pre_buf + ((c0 - cbeg) / 16) % C::kPreBufs * (C::kPreBlockBytes / (int)sizeof(OutT));
-            };
-            if (!it.split) pre_begin();  // a split tile: only the block that finishes it reads them
+            if (!it.split) pre_fetch(cbeg);  // a split tile: only the block that finishes it reads them
             // every epilogue thread goes on, or all leave (the split path below
             // meets at named barriers, which a thread that left would never reach)
             const bool got = mbar_wait_bounded(&tfull[b], aph, deadline, abort_flag);
@@ -761,7 +757,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if constexpr (kEpi == kEpiSwiGLUTrain || kEpi == kEpiSwiGLUGrad)
                 prow = reinterpret_cast<OutT*>(p.pre) + (long long)t.row0 * 2 * p.n_out + f;
             const int n_out = p.n_out;
-            auto emit = [orow, prow, n_out, nrows, out_ld, v0, v1, lane, &pre_next](int c0, float (&g)[16], float (&u)[16]) {
+            auto emit = [orow, prow, n_out, nrows, out_ld, v0, v1, &pre, &pre_fetch](int c0, float (&g)[16], float (&u)[16]) {
                 const int n = nrows - c0 < 16 ? nrows - c0 : 16;
                 if constexpr (kEpi == kEpiSwiGLUTrain) {
                     if (v0) {
@@ -778,17 +774,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     return;
                 }
                 if constexpr (kEpi == kEpiSwiGLUGrad) {
-                    // this lane's feature of the block read ahead, 16 tokens of gate, then of up
-                    const OutT* pb = pre_next(c0) + lane;
+                    float pg[16], pu[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        pg[i] = __uint_as_float((uint32_t)pre[i] << 16);
+                        pu[i] = __uint_as_float((uint32_t)pre[16 + i] << 16);
+                    }
+                    pre_fetch(c0 + 16);
                     if (v0) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             if (i < n) {
-                                const float pg = Elt<OutT>::to_f(pb[i * 32]), pu = Elt<OutT>::to_f(pb[(16 + i) * 32]);
-                                const float sg = __fdividef(1.f, 1.f + __expf(-pg));
+                                const float sg = __fdividef(1.f, 1.f + __expf(-pg[i]));
                                 OutT* o = orow + (c0 + i) * out_ld;
-                                store_out<OutT>(o, g[i] * pu * sg * (1.f + pg * (1.f - sg)));
-                                store_out<OutT>(o + n_out, g[i] * pg * sg);
+                                store_out<OutT>(o, g[i] * pu[i] * sg * (1.f + pg[i] * (1.f - sg)));
+                                store_out<OutT>(o + n_out, g[i] * pg[i] * sg);
                             }
                         }
                     }
@@ -931,7 +931,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
                 if (arrived == ncontrib - 1) {
                     // last to arrive: sum every contribution in block order, then the epilogue
-                    pre_begin();
+                    pre_fetch(cbeg);
                     for (int c0 = cbeg; c0 < cend; c0 += 16) {
                         float g[16], u[16];
 #pragma unroll
@@ -1002,7 +1002,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             }
             ++ac;
         }
-        if constexpr (kEpi == kEpiSwiGLUGrad) cp_async_wait<0>();
     }
 
     tc_fence_before();

@@ -137,13 +137,16 @@ int launch_variant(const GemmLaunch& L, const GemmCtl& ctl, int num_sms, cudaStr
     CUtensorMap tm_w, tm_x, tm_x64, tm_xbig;
     constexpr int rb = C::kRowBytes;
     const bool joined = kWMn && kCta == 2 && L.n_out % 64 == 0;
-    if (joined ? !make_map_cols(&tm_w, Elt<T>::kTma, L.w, L.n_groups, L.kdim, L.n_out, C::kBK, 2 * C::kNW)
-        : kWMn ? !make_map3(&tm_w, Elt<T>::kTma, Elt<T>::kBytes, L.w, L.n_groups, L.kdim, L.n_out, C::kBK)
+    if (joined ? !make_map_cols(&tm_w, Elt<T>::kTma, L.w, L.n_groups, L.kdim, L.n_out, C::kStageK, 2 * C::kNW)
+        : kWMn ? !make_map3(&tm_w, Elt<T>::kTma, Elt<T>::kBytes, L.w, L.n_groups, L.kdim, L.n_out, C::kStageK)
              : !make_map(&tm_w, Elt<T>::kTma, Elt<T>::kBytes, L.w, L.w_rows, L.kdim, 128, rb))
         return -3;
-    if (!make_map(&tm_x, Elt<T>::kTma, Elt<T>::kBytes, L.x, L.x_rows, L.kdim, C::kXBoxRows, rb)) return -3;
-    if (!make_map(&tm_x64, Elt<T>::kTma, Elt<T>::kBytes, L.x, L.x_rows, L.kdim, C::kXBoxMid, rb)) return -3;
-    if (!make_map(&tm_xbig, Elt<T>::kTma, Elt<T>::kBytes, L.x, L.x_rows, L.kdim, kMaxN / kCta, rb)) return -3;
+    const bool x_joined = C::kChunks > 1 && L.kdim % C::kBK == 0;
+    auto x_map = [&](CUtensorMap* m, int rows) {
+        if (x_joined) return make_map_cols(m, Elt<T>::kTma, L.x, 1, L.x_rows, L.kdim, rows, C::kChunks);
+        return make_map(m, Elt<T>::kTma, Elt<T>::kBytes, L.x, L.x_rows, L.kdim, rows, rb);
+    };
+    if (!x_map(&tm_x, C::kXBoxRows) || !x_map(&tm_x64, C::kXBoxMid) || !x_map(&tm_xbig, kMaxN / kCta)) return -3;
     GemmParams p;
     p.seg_offsets = L.seg_offsets;
     p.n_groups = L.n_groups;
@@ -156,6 +159,7 @@ int launch_variant(const GemmLaunch& L, const GemmCtl& ctl, int num_sms, cudaStr
     p.out_ld = L.out_ld;
     p.pre = L.pre;
     p.w_joined = joined ? 1 : 0;
+    p.x_joined = x_joined ? 1 : 0;
     p.counters = ctl.counters;
     p.partials = ctl.partials;
     p.status = ctl.status;
@@ -165,7 +169,7 @@ int launch_variant(const GemmLaunch& L, const GemmCtl& ctl, int num_sms, cudaStr
     // whose partial sums take longer than that to add up (8 experts of 1024 x
     // 1024, 512 tokens, down gradient: 28 us whole, 39 us in slices of 4; with 8
     // tokens in all, gate/up gradient: 25 us whole, 18 us in slices)
-    p.sk_min_units = kTrain && L.x_rows > 64LL * L.n_groups ? 16 : 4;
+    p.sk_min_units = kTrain && L.x_rows > 64LL * L.n_groups ? 16 / C::kChunks : 4 / C::kChunks;
     p.max_split = L.max_split > 0 ? L.max_split : 4;
     p.split_tail = split_tail_mode();
     int grid = grid_blocks;
