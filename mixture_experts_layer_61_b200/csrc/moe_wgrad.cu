@@ -14,14 +14,13 @@
 // operands.  Reads from L2 and writes share the SMs' way to it (a copy kernel
 // with this kernel's loads and stores takes the sum of their times), so an
 // expert of up to 256 rows keeps its 128 columns of d in shared memory over a
-// run of tiles and streams only x.  The epilogue packs bf16 into a swizzled
-// shared-memory block per warp and stores it by TMA, which clips at the
-// weight's own edges.
+// run of tiles and streams only x.  The epilogue packs bf16 into swizzled
+// shared memory and stores it by TMA, which clips at the weight's own edges.
 //
 // Qwen2-MoE-shaped gate/up weights (64 x 5120 x 3584, 16384 rows, experts very
-// uneven): 740 us, 2.35 GB written and 0.6 TFLOP; with even experts of at most
-// 256 rows (12800 rows) 625 us.  The first version, d and x streamed for
-// every tile and one staging block per warp, took 968 us.
+// uneven): 725 us, 2.35 GB written and 0.6 TFLOP; with even experts of at most
+// 256 rows (12800 rows) 590 us.  The first version, d and x streamed for
+// every tile and one 4 KB staging block per warp, took 968 us.
 //
 // Segments are whole multiples of 16 rows (the MMA's K), their padding rows
 // zero in both operands; a stage reads up to 63 rows past its segment, but
@@ -139,7 +138,8 @@ struct WgSched {
 
 __global__ void __launch_bounds__(kWgThreads, 1)
     moe_wgrad_kernel(const __grid_constant__ CUtensorMap tm_d, const __grid_constant__ CUtensorMap tm_x,
-                     const __grid_constant__ CUtensorMap tm_out, const WgradParams p) {
+                     const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_out128,
+                     const WgradParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* panel = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* ring = panel + kWgPanel * kWgOperandBytes;
@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         tma_prefetch_desc(&tm_d);
         tma_prefetch_desc(&tm_x);
         tma_prefetch_desc(&tm_out);
+        tma_prefetch_desc(&tm_out128);
     }
     if (warp == 1) tmem_alloc_pair(tmem_holder, 512);
     cluster_sync_all();  // the peer's barriers are initialised before any TMA or commit targets them
@@ -337,13 +338,14 @@ __global__ void __launch_bounds__(kWgThreads, 1)
         uint8_t* mine = store_base + (warp - 2) * kWgStoreBytes;
         const uint64_t pol_out = policy_evict_first();  // written once: the operands keep L2
         uint32_t ac = 0;
-        bool ok = true;
+        bool ok = true, was_together = false;
         while (ok && sch.next(it)) {
             for (int j = 0; j < it.tiles; ++j) {
                 const int b = ac & 1;
                 if (it.steps > 0) {
+                    // a half's warps meet at barriers below: all go on, or all leave
                     const bool got = mbar_wait_bounded(&tfull[b], (ac >> 1) & 1u, p.wait_limit_ns, abort_flag);
-                    if (!__all_sync(0xffffffffu, got)) {
+                    if (!named_all(1 + half, 128, got)) {
                         *abort_flag = 1;
                         if (lane == 0) atomicOr(p.status, kStatusTimeout);
                         ok = false;
@@ -381,24 +383,41 @@ __global__ void __launch_bounds__(kWgThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 64; ++i) w[i] = 0u;
                 }
-                if (lane == 0) bulk_wait_read();  // the last tile's stores have read this warp's blocks
-                __syncwarp();
+                // more than 64 rows, columns in whole blocks of 64: the half's four warps
+                // store 128 x 128 in one copy (a copy costs the TMA unit 65 ns and 0.7 ns
+                // a 128-byte row; with a copy a warp, stores took a third of a tile's time:
+                // 12800 rows in 64 experts, 627 us against 590 us).  Few rows are bound by
+                // the epilogue's latency: a warp stores its own 32 rows without meeting the
+                // others (512 rows in 64 experts: 414 us against 430 us)
+                const bool together = p.x_joined && it.steps > 4;
+                uint8_t* blk = together ? store_base + half * (4 * kWgStoreBytes) + quad * (32 * 128) : mine;
+                const int chunk = together ? 128 * 128 : 32 * 128;  // from one 64-column block to the next
+                if (lane == 0) bulk_wait_read();  // this thread's stores have read the staging
+                if (together || was_together) named_sync(1 + half, 128);
+                else __syncwarp();
+                was_together = together;
 #pragma unroll
                 for (int q = 0; q < 16; ++q)
-                    *reinterpret_cast<int4*>(mine + (q >> 3) * (kWgStoreBytes / 2) + lane * 128 +
-                                             (((q & 7) ^ (lane & 7)) * 16)) =
+                    *reinterpret_cast<int4*>(blk + (q >> 3) * chunk + lane * 128 + (((q & 7) ^ (lane & 7)) * 16)) =
                         make_int4((int)w[4 * q], (int)w[4 * q + 1], (int)w[4 * q + 2], (int)w[4 * q + 3]);
                 fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0 && row < p.m) {
-                    if (p.x_joined) {
-                        if (col < p.n) tma_store_4d(&tm_out, mine, 0, row, col / 64, it.g, pol_out);
-                    } else {
-                        if (col < p.n) tma_store_3d(&tm_out, mine, col, row, it.g, pol_out);
-                        if (col + 64 < p.n)
-                            tma_store_3d(&tm_out, mine + kWgStoreBytes / 2, col + 64, row, it.g, pol_out);
+                if (together) {
+                    named_sync(1 + half, 128);
+                    if (lane == 0 && quad == 0 && row < p.m && col < p.n) {
+                        tma_store_4d(&tm_out128, blk, 0, row, col / 64, it.g, pol_out);
+                        bulk_commit();
                     }
-                    bulk_commit();
+                } else {
+                    __syncwarp();
+                    if (lane == 0 && row < p.m) {
+                        if (p.x_joined) {
+                            if (col < p.n) tma_store_4d(&tm_out, blk, 0, row, col / 64, it.g, pol_out);
+                        } else {
+                            if (col < p.n) tma_store_3d(&tm_out, blk, col, row, it.g, pol_out);
+                            if (col + 64 < p.n) tma_store_3d(&tm_out, blk + chunk, col + 64, row, it.g, pol_out);
+                        }
+                        bulk_commit();
+                    }
                 }
             }
         }
@@ -424,14 +443,16 @@ int launch_wgrad(const WgradLaunch& L, const GemmCtl& ctl, cudaStream_t stream) 
     static std::atomic<int> cache[kMaxCachedDevices];
     int blocks = 0;
     if ((rc = resident_blocks(moe_wgrad_kernel, kWgSmemBytes, kWgThreads, 2, d, cache, &blocks)) != 0) return rc;
-    CUtensorMap tm_d, tm_x, tm_out;
+    CUtensorMap tm_d, tm_x, tm_out, tm_out128;
     const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     const int dj = L.m % 64 == 0, xj = L.n % 64 == 0;
     if (!(dj ? make_map_cols(&tm_d, dt, L.d, 1, L.rows, L.m, kWgBK, 2) : make_map(&tm_d, dt, 2, L.d, L.rows, L.m, kWgBK)) ||
         !(xj ? make_map_cols(&tm_x, dt, L.x, 1, L.rows, L.n, kWgBK, 2) : make_map(&tm_x, dt, 2, L.x, L.rows, L.n, kWgBK)) ||
-        !(xj ? make_map_cols(&tm_out, dt, L.out, L.n_groups, L.m, L.n, 32, 2)
+        !(xj ? make_map_cols(&tm_out, dt, L.out, L.n_groups, L.m, L.n, 32, 2) &&
+                   make_map_cols(&tm_out128, dt, L.out, L.n_groups, L.m, L.n, 128, 2)
              : make_map3(&tm_out, dt, 2, L.out, L.n_groups, L.m, L.n, 32)))
         return -3;
+    if (!xj) tm_out128 = tm_out;  // not used
     const long long n_tiles = (L.n + 255) / 256, tiles = (long long)((L.m + 255) / 256) * n_tiles;
     if (tiles * L.n_groups > 0x7fffffffLL - d.num_sms) return -1;
     if (2 * tiles * L.n_groups < blocks) blocks = (int)(2 * tiles * L.n_groups);
@@ -441,7 +462,7 @@ int launch_wgrad(const WgradLaunch& L, const GemmCtl& ctl, cudaStream_t stream) 
     WgradParams p{L.seg_offsets, L.n_groups, L.m, L.n, dj, xj, (int)run, ctl.status, wait_limit_ns(),
                   take_withhold_flag()};
     const cudaError_t e = launch_kernel_cluster(moe_wgrad_kernel, dim3(blocks), dim3(kWgThreads), kWgSmemBytes, stream,
-                                                2, tm_d, tm_x, tm_out, p);
+                                                2, tm_d, tm_x, tm_out, tm_out128, p);
     count_launch();
     if (e != cudaSuccess) cudaGetLastError();
     return e == cudaSuccess ? 0 : -3;
