@@ -544,7 +544,8 @@ int moe_route_grad(const moe_config_t* cfg, const float* logits, const int32_t* 
  * the activation dtype.  y NULL: only the norm before a block (h =
  * res_scale * residual; no w_post or gate then).  residual NULL: none.  n is
  * given with w_next and only then; h may be NULL beside n.  n is computed
- * from h before its rounding.  h may be residual or y itself (in place). */
+ * from h before its rounding.  h may be residual or y itself (in place).  The
+ * mean squares are fp32: a row whose squares leave its range norms to zero. */
 int moe_block_norm(const moe_norm_config_t* nc, const void* y, const void* residual, const void* w_post,
                    const void* gate, const void* w_next, void* h, void* n, moe_stream_t stream);
 

@@ -114,11 +114,10 @@ int check_norm_args(const moe_norm_config_t* c, const void* y, const void* resid
 
 // The training products' common checks: bf16, segments in whole MMA steps of
 // 16 rows (the weight gradients reduce over them).
-int check_train(const moe_config_t* cfg, const void* workspace) {
+int check_train(const moe_config_t* cfg) {
     int rc = check_cfg(cfg);
     if (rc) return rc;
-    if (cfg->dtype != 0 || cfg->tile_B % 16 != 0 || !workspace || !aligned16(workspace)) return MOE_ERR_ARG;
-    return MOE_OK;
+    return cfg->dtype != 0 || cfg->tile_B % 16 != 0 ? MOE_ERR_ARG : MOE_OK;
 }
 
 long long p_max(const moe_config_t* c) {
@@ -684,7 +683,7 @@ int moe_block_norm_grad(const moe_norm_config_t* nc, const void* h, const void* 
     for (const void* p : {h, dh, dn, y, w_post, gate, w_next, (const void*)dresidual, (const void*)dy,
                           (const void*)dgate, (const void*)dw_post, (const void*)dw_next, (const void*)workspace})
         if (!aligned16(p)) return MOE_ERR_ARG;
-    if (!workspace) return MOE_ERR_ARG;
+    if (rows && !workspace) return MOE_ERR_ARG;
     DeviceInfo d;
     if ((rc = current_device(&d)) != 0) return status_of(rc);
     if (ws_bytes < (size_t)norm_grad_blocks(nc->T, nc->H, nc->dtype, d.num_sms) * 2 * nc->H * sizeof(float)) return MOE_ERR_WORKSPACE;
@@ -695,9 +694,10 @@ int moe_block_norm_grad(const moe_norm_config_t* nc, const void* h, const void* 
 
 int moe_grouped_gate_up_train(const moe_config_t* cfg, const void* x_perm, const void* w13, const int32_t* offsets,
                               void* h13, void* act, void* workspace, size_t ws_bytes, moe_stream_t stream) {
-    int rc = check_train(cfg, workspace);
+    int rc = check_train(cfg);
     if (rc) return rc;
     if (cfg->T == 0) return MOE_OK;
+    if (!workspace || !aligned16(workspace)) return MOE_ERR_ARG;
     if (!x_perm || !w13 || !offsets || !h13 || !act) return MOE_ERR_ARG;
     if (!aligned16(x_perm) || !aligned16(w13) || !aligned16(h13) || !aligned16(act)) return MOE_ERR_ARG;
     DeviceInfo d;
@@ -710,9 +710,10 @@ int moe_grouped_gate_up_train(const moe_config_t* cfg, const void* x_perm, const
 
 int moe_grouped_down_grad(const moe_config_t* cfg, const void* dy_perm, const void* w2, const void* h13,
                           const int32_t* offsets, void* dh13, void* workspace, size_t ws_bytes, moe_stream_t stream) {
-    int rc = check_train(cfg, workspace);
+    int rc = check_train(cfg);
     if (rc) return rc;
     if (cfg->T == 0) return MOE_OK;
+    if (!workspace || !aligned16(workspace)) return MOE_ERR_ARG;
     if (!dy_perm || !w2 || !h13 || !offsets || !dh13) return MOE_ERR_ARG;
     if (!aligned16(dy_perm) || !aligned16(w2) || !aligned16(h13) || !aligned16(dh13)) return MOE_ERR_ARG;
     DeviceInfo d;
@@ -735,9 +736,10 @@ int moe_grouped_down_grad(const moe_config_t* cfg, const void* dy_perm, const vo
 
 int moe_grouped_gate_up_grad(const moe_config_t* cfg, const void* dh13, const void* w13, const int32_t* offsets,
                              void* dx_perm, void* workspace, size_t ws_bytes, moe_stream_t stream) {
-    int rc = check_train(cfg, workspace);
+    int rc = check_train(cfg);
     if (rc) return rc;
     if (cfg->T == 0) return MOE_OK;
+    if (!workspace || !aligned16(workspace)) return MOE_ERR_ARG;
     if (!dh13 || !w13 || !offsets || !dx_perm) return MOE_ERR_ARG;
     if (!aligned16(dh13) || !aligned16(w13) || !aligned16(dx_perm)) return MOE_ERR_ARG;
     DeviceInfo d;
@@ -760,13 +762,15 @@ int moe_grouped_gate_up_grad(const moe_config_t* cfg, const void* dh13, const vo
 namespace {
 int wgrad(const moe_config_t* cfg, const void* d_rows, int m, const void* x_rows, int n, const int32_t* offsets,
           void* out, void* workspace, size_t ws_bytes, moe_stream_t stream) {
-    int rc = check_train(cfg, workspace);
+    int rc = check_train(cfg);
     if (rc) return rc;
     if (!out || !aligned16(out)) return MOE_ERR_ARG;
-    if (cfg->T > 0 && (!d_rows || !x_rows || !offsets || !aligned16(d_rows) || !aligned16(x_rows))) return MOE_ERR_ARG;
+    if (cfg->T > 0 && (!d_rows || !x_rows || !offsets || !workspace || !aligned16(d_rows) || !aligned16(x_rows) ||
+                       !aligned16(workspace)))
+        return MOE_ERR_ARG;
     DeviceInfo d;
     if ((rc = current_device(&d)) != 0) return status_of(rc);
-    if (ws_bytes < ctl_block_bytes(d.num_sms)) return MOE_ERR_WORKSPACE;
+    if (cfg->T > 0 && ws_bytes < ctl_block_bytes(d.num_sms)) return MOE_ERR_WORKSPACE;
     if (cfg->T == 0) {
         const cudaError_t e = cudaMemsetAsync(out, 0, (size_t)2 * cfg->E * m * n, (cudaStream_t)stream);
         if (e != cudaSuccess) cudaGetLastError();

@@ -379,8 +379,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     constexpr bool kTrain = kWMn || kEpi == kEpiSwiGLUTrain;
     using C = GemmCfg<T, kEpi, kMaxN, kCta, kTrain>;
     constexpr bool kSwiGLU = kEpi == kEpiSwiGLU || kEpi == kEpiSwiGLUTrain;
-    static_assert(!kWMn || (Elt<T>::kBytes == 2 && C::kBK == 64), "MN-major weights: 16-bit, 64 features per box row");
-    static_assert(C::kChunks == 1 || (kWMn && kCta == 2), "stages of several chunks: MN-major weights on pairs");
+    static_assert(!kWMn || (kCta == 2 && Elt<T>::kBytes == 2 && C::kBK == 64), "MN-major weights: 16-bit, on pairs");
+    static_assert(C::kChunks == 1 || kWMn, "stages of several k-chunks: MN-major weights");
     constexpr bool kTwo = C::kNW == 2;
     constexpr bool kPair = kCta == 2;
     extern __shared__ uint8_t smem_raw[];
@@ -535,19 +535,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         else tma_load_2d(dst, m, &full[s], k * C::kBK, c1, pol);
                     };
                     if constexpr (kWMn) {
-                        // boxes of 64 features by kBK rows of K; K rows past kdim read as zero
+                        // boxes of 64 features by kStageK rows of K; K rows past kdim read as zero
                         const int f0 = t.f0 + (int)rank * C::kFeat;
-                        if (kPair && p.w_joined)
+                        if (p.w_joined)
                             tma_load_4d_pair(st, &tm_w, fb, 0, k * C::kStageK, f0 / 64, t.group, pol_w);
                         else
 #pragma unroll
-                        for (int b = 0; b < 2 * C::kNW; ++b) {
-                            uint8_t* dst = st + b * (C::kStageK * 128);
-                            if (kPair)
-                                tma_load_3d_pair(dst, &tm_w, fb, f0 + 64 * b, k * C::kStageK, t.group, pol_w);
-                            else
-                                tma_load_3d(dst, &tm_w, &full[s], f0 + 64 * b, k * C::kStageK, t.group, pol_w);
-                        }
+                            for (int b = 0; b < 2 * C::kNW; ++b)
+                                tma_load_3d_pair(st + b * (C::kStageK * 128), &tm_w, fb, f0 + 64 * b, k * C::kStageK,
+                                                 t.group, pol_w);
                     } else {
                         load(st, &tm_w, wrow, pol_w);
                         if (kTwo) load(st + C::kWTileBytes, &tm_w, wrow + (kSwiGLU ? p.up_offset : 128), pol_w);

@@ -161,6 +161,9 @@ def test_zero_tokens_is_a_no_op_without_pointers():
         assert call(name, cfg(T=0), [NONE] * CALLS[name][0]) == 0
     for name in ("moe_grouped_gate_up_train", "moe_grouped_down_grad", "moe_grouped_gate_up_grad"):
         assert call(name, cfg(T=0), [NONE] * CALLS[name][0]) == 0
+        assert call(name, cfg(T=0), [NONE] * CALLS[name][0], ws=NONE) == 0
+    for name in ("moe_grouped_down_wgrad", "moe_grouped_gate_up_wgrad"):  # these write zeros: somewhere
+        assert call(name, cfg(T=0), [NONE] * 4) == ARG
     assert norm(nc(T=0), y=NONE, residual=NONE, h=NONE) == 0
     assert combine_norm(cfg(T=0), nc(T=0), y=NONE, pos=NONE, w=NONE, residual=NONE, h=NONE) == 0
 
