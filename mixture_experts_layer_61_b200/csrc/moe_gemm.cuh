@@ -692,13 +692,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             }
             auto pre_fetch = [&](int c0) {
                 if constexpr (kEpi == kEpiSwiGLUGrad) {
+                    auto get = [&](int i) {
+                        const uint16_t* q = pre_in + (long long)(c0 + i) * 2 * p.n_out;
+                        pre[i] = q[0];
+                        pre[16 + i] = q[p.n_out];
+                    };
+                    if (pre_in && c0 + 16 <= cend) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if (pre_in && c0 + i < cend) {
-                            const uint16_t* q = pre_in + (long long)(c0 + i) * 2 * p.n_out;
-                            pre[i] = q[0];
-                            pre[16 + i] = q[p.n_out];
-                        }
+                        for (int i = 0; i < 16; ++i) get(i);
+                    } else if (pre_in) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c0 + i < cend) get(i);
                     }
                 }
             };
@@ -756,16 +761,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             auto emit = [orow, prow, n_out, nrows, out_ld, v0, v1, &pre, &pre_fetch](int c0, float (&g)[16], float (&u)[16]) {
                 const int n = nrows - c0 < 16 ? nrows - c0 : 16;
                 if constexpr (kEpi == kEpiSwiGLUTrain) {
-                    if (v0) {
+                    auto put = [&](int i) {
+                        OutT* pr = prow + (long long)(c0 + i) * 2 * n_out;
+                        store_out<OutT>(pr, g[i]);
+                        store_out<OutT>(pr + n_out, u[i]);
+                        store_out<OutT>(orow + (c0 + i) * out_ld, silu_mul(g[i], u[i]));
+                    };
+                    if (v0 && n == 16) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            if (i < n) {
-                                OutT* pr = prow + (long long)(c0 + i) * 2 * n_out;
-                                store_out<OutT>(pr, g[i]);
-                                store_out<OutT>(pr + n_out, u[i]);
-                                store_out<OutT>(orow + (c0 + i) * out_ld, silu_mul(g[i], u[i]));
-                            }
-                        }
+                        for (int i = 0; i < 16; ++i) put(i);
+                    } else if (v0) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (i < n) put(i);
                     }
                     return;
                 }
@@ -777,16 +785,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         pu[i] = __uint_as_float((uint32_t)pre[16 + i] << 16);
                     }
                     pre_fetch(c0 + 16);
-                    if (v0) {
+                    auto put = [&](int i) {
+                        const float sg = __fdividef(1.f, 1.f + __expf(-pg[i]));
+                        OutT* o = orow + (c0 + i) * out_ld;
+                        store_out<OutT>(o, g[i] * pu[i] * sg * (1.f + pg[i] * (1.f - sg)));
+                        store_out<OutT>(o + n_out, g[i] * pg[i] * sg);
+                    };
+                    if (v0 && n == 16) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            if (i < n) {
-                                const float sg = __fdividef(1.f, 1.f + __expf(-pg[i]));
-                                OutT* o = orow + (c0 + i) * out_ld;
-                                store_out<OutT>(o, g[i] * pu[i] * sg * (1.f + pg[i] * (1.f - sg)));
-                                store_out<OutT>(o + n_out, g[i] * pg[i] * sg);
-                            }
-                        }
+                        for (int i = 0; i < 16; ++i) put(i);
+                    } else if (v0) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (i < n) put(i);
                     }
                     return;
                 }
