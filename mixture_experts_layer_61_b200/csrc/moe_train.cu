@@ -111,7 +111,7 @@ constexpr int kMaxCachedDevices = 64;
 
 }  // namespace
 
-bool row_kernels_fit(int H, int dtype) { return H * (dtype == 0 ? 2 : 4) <= 32 * 1024; }
+bool row_kernels_fit(int H, int dtype) { return H <= 32 * 1024 / (dtype == 0 ? 2 : 4); }
 
 // ------------------------------------------------------------- block norm
 // For one token:  y = the block's output (given, or the combine's weighted sum

@@ -203,3 +203,16 @@ def test_binding_refuses_tensors_that_do_not_fit():
                     Fake((32, 256), torch.bfloat16, contiguous=False), Fake((32, 256), torch.bfloat16, index=1)):
             with pytest.raises(ValueError):
                 moe._arg("x", bad, (32, 256), torch.bfloat16)
+
+
+WRAPPING = [(1 << 30, moe.FP32), ((1 << 30) + 4, moe.FP32), (1 << 30, moe.BF16), ((1 << 30) + 8, moe.BF16)]
+
+
+@pytest.mark.parametrize("H,dtype", WRAPPING)
+def test_row_bytes_past_32_bits_are_refused(H, dtype):
+    """Rows whose bytes, as a 32-bit number, wrap to a short or negative row."""
+    c = nc(T=1, H=H, dtype=dtype)
+    assert norm(c) == ARG and norm_grad(c) == ARG
+    k = cfg(T=1, E=1, K=1, H=H, I=8, dtype=dtype)
+    assert combine_norm(k, c) == ARG
+    assert call("moe_combine_grad", k, [P] * 8) == ARG
