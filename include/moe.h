@@ -579,8 +579,8 @@ int moe_block_norm_grad(const moe_norm_config_t* nc, const void* h, const void* 
                         moe_stream_t stream);
 
 /* The experts' products of a training step, bf16 only (cfg->dtype 0), tile_B
- * a multiple of 16 (MOE_ERR_ARG otherwise): segments are then whole tensor-core
- * steps of 16 rows.  Workspace and its status as for moe_grouped_ffn
+ * a multiple of 16, H and 2 I at most 2^30 (MOE_ERR_ARG otherwise): segments
+ * are then whole tensor-core steps of 16 rows.  Workspace and its status as for moe_grouped_ffn
  * (moe_gemm_workspace_size(), moe_check_status).  Padding rows of the row
  * buffers must be zero, as moe_permute, moe_combine_grad and these calls
  * leave them.

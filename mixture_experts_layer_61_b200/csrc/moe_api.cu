@@ -117,7 +117,9 @@ int check_norm_args(const moe_norm_config_t* c, const void* y, const void* resid
 int check_train(const moe_config_t* cfg) {
     int rc = check_cfg(cfg);
     if (rc) return rc;
-    return cfg->dtype != 0 || cfg->tile_B % 16 != 0 ? MOE_ERR_ARG : MOE_OK;
+    if (cfg->dtype != 0 || cfg->tile_B % 16 != 0) return MOE_ERR_ARG;
+    // tile coordinates, which run past the last column by less than a tile, are 32-bit
+    return cfg->H > (1 << 30) || cfg->I > (1 << 29) ? MOE_ERR_ARG : MOE_OK;
 }
 
 long long p_max(const moe_config_t* c) {

@@ -216,3 +216,9 @@ def test_row_bytes_past_32_bits_are_refused(H, dtype):
     k = cfg(T=1, E=1, K=1, H=H, I=8, dtype=dtype)
     assert combine_norm(k, c) == ARG
     assert call("moe_combine_grad", k, [P] * 8) == ARG
+
+
+@pytest.mark.parametrize("name", [n for n in CALLS if n.startswith("moe_grouped")])
+@pytest.mark.parametrize("size", [dict(H=(1 << 30) + 8, I=8), dict(H=8, I=(1 << 29) + 8), dict(H=8, I=(1 << 30) - 8)])
+def test_products_whose_tile_coordinates_would_pass_32_bits_are_refused(name, size):
+    assert call(name, cfg(T=1, E=1, K=1, **size), [P] * CALLS[name][0]) == ARG
