@@ -63,9 +63,10 @@ __device__ __forceinline__ float warp_sum8(const float (&v)[8], int lane) {
     return c;
 }
 
-// Eight sums over the block, given to every thread.  `buf` is [32][8] floats;
-// two calls may not share it without a barrier in between (callers alternate
-// two buffers, so one barrier per call is enough).
+// Eight sums over the block, given to every thread.  `buf` is [32][8] floats,
+// zero past the block's warps, so that sixteen warps' are read at once; two
+// calls may not share it without a barrier in between (callers alternate two
+// buffers, so one barrier per call is enough).
 __device__ __forceinline__ void block_sum8(float (&v)[8], float* buf) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     float c = warp_sum8(v, lane);
@@ -73,7 +74,9 @@ __device__ __forceinline__ void block_sum8(float (&v)[8], float* buf) {
         if (lane < 8) buf[warp * 8 + lane] = c;
         __syncthreads();
         c = 0.f;
-        for (int w = lane >> 3; w < nw; w += 4) c += buf[w * 8 + (lane & 7)];
+        for (int w0 = 0; w0 < nw; w0 += 16)
+#pragma unroll
+            for (int w = 0; w < 16; w += 4) c += buf[(w0 + w) * 8 + lane];
         c += __shfl_xor_sync(0xffffffffu, c, 8);
         c += __shfl_xor_sync(0xffffffffu, c, 16);
     }
@@ -295,8 +298,8 @@ int launch_block_norm(const BlockNormArgs& a, cudaStream_t stream) {
 // tested in the loops it made 990 instructions of a vector's 300.  Persistent
 // blocks take tokens block-stride; their column sums go to the workspace as
 // one fp32 row per block and are added in block order by norm_wgrad_kernel:
-// deterministic.  4096 tokens of 7168 bf16 with every part: 91 us, 352 MB (0.60
-// of the copy bandwidth; issue slots 63 % used); 448 threads holding rows in
+// deterministic.  4096 tokens of 7168 bf16 with every part: 87 us, 352 MB (0.63
+// of the copy bandwidth; issue slots 61 % used); 448 threads holding rows in
 // registers took 131 us.
 
 // Two floats in a register pair, and operations on both (each rounded as the
@@ -386,7 +389,17 @@ __global__ void __launch_bounds__(kNormGradThreads) block_norm_grad_kernel(Block
     const float inv_h = 1.f / a.H;
     const T* tag = nullptr;
     const f2 zero2 = f2_both(0.f);
-    float4* coef = reinterpret_cast<float4*>(smem);  // quad q of vector v at [v * kQ + q]
+    for (int i = tid; i < 2 * 32 * 8; i += nt)
+        if ((i & 255) >= nt / 4) red[i >> 8][i & 255] = 0.f;  // warps the block has not: read by block_sum8
+    float4* coef = reinterpret_cast<float4*>(smem);  // quad q of vector v at [q * stream + v]
+    // Every other eight lanes take their two quads of a bf16 vector the other way
+    // round, so that sixteen lanes' 8-byte reads, 16 bytes apart, meet all banks
+    // once: quad k of a thread (the index of its sums) is quad k ^ swap of the
+    // vector.  Where shared memory is what is waited for: with a gate per token,
+    // and in rows past 16 KB (4096 x 7168, token gate: 111 us without, 104 us; 2048
+    // x 16384: 145 us, 137 us); elsewhere the added address arithmetic costs more
+    // (32768 x 2048: 158 us without, 164 us)
+    const int swap = kQ == 2 && (kGate == 2 || kV == 2) ? (tid >> 3) & 1 : 0;
     int4* wnext = smem + S::kCoef * stream;
     int4* rows = smem + S::kHead * stream;
     const int stage_vec = S::kIn * stream;
@@ -427,7 +440,7 @@ __global__ void __launch_bounds__(kNormGradThreads) block_norm_grad_kernel(Block
         }
     };
     auto get_coef = [&](int v, int q, f2 (&c)[2]) {
-        if (S::kHeld) quad(reinterpret_cast<const int4*>(coef + v * kQ + q), 0, c, (const float*)nullptr);
+        if (S::kHeld) quad(reinterpret_cast<const int4*>(coef + q * stream + v), 0, c, (const float*)nullptr);
         else coef_of(v, q, c);
     };
     auto get_wnext = [&](int v, int q, f2 (&f)[2]) {
@@ -451,7 +464,7 @@ __global__ void __launch_bounds__(kNormGradThreads) block_norm_grad_kernel(Block
                     float4 x;
                     f2_split(c[0], x.x, x.y);
                     f2_split(c[1], x.z, x.w);
-                    coef[v * kQ + q] = x;
+                    coef[q * stream + v] = x;
                 }
             }
             if (S::kHeld && kNext) wnext[v] = __ldg(static_cast<const int4*>(a.w_next) + v);
@@ -471,7 +484,8 @@ __global__ void __launch_bounds__(kNormGradThreads) block_norm_grad_kernel(Block
             const int v = tid + j * nt;
             if (v < row_vec) {
 #pragma unroll
-                for (int q = 0; q < kQ; ++q) {
+                for (int k = 0; k < kQ; ++k) {
+                    const int q = k ^ swap;
                     f2 h[2], dn[2], c[2], f[2];
                     if (kNext) {
                         quad(row + S::kH * stream + v, q, h, tag);
@@ -528,7 +542,8 @@ __global__ void __launch_bounds__(kNormGradThreads) block_norm_grad_kernel(Block
             if (v < row_vec) {
                 const long long o = t * row_vec + v;
 #pragma unroll
-                for (int q = 0; q < kQ; ++q) {
+                for (int k = 0; k < kQ; ++k) {
+                    const int q = k ^ swap;
                     f2 d[2], x[2], f[2], g[2];
                     quad(row + S::kDh * stream + v, q, d, tag);
                     if (kNext) {
@@ -538,7 +553,7 @@ __global__ void __launch_bounds__(kNormGradThreads) block_norm_grad_kernel(Block
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             g[i] = f2_mul(g[i], rh);
-                            acc_next[j][2 * q + i] = f2_fma(g[i], x[i], acc_next[j][2 * q + i]);
+                            acc_next[j][2 * k + i] = f2_fma(g[i], x[i], acc_next[j][2 * k + i]);
                             d[i] = f2_fma(f[i], g[i], d[i]);
                             d[i] = f2_fma(mh, x[i], d[i]);
                         }
@@ -559,10 +574,10 @@ __global__ void __launch_bounds__(kNormGradThreads) block_norm_grad_kernel(Block
                             if (kGate == 2) {
                                 const f2 e = f2_mul(d[i], x[i]);  // d y rho_y
                                 dg[i] = f2_mul(e, f[i]);
-                                acc_post[j][2 * q + i] = f2_fma(g[i], e, acc_post[j][2 * q + i]);
+                                acc_post[j][2 * k + i] = f2_fma(g[i], e, acc_post[j][2 * k + i]);
                                 d[i] = f2_mul(d[i], g[i]);
                             } else {
-                                acc_post[j][2 * q + i] = f2_fma(d[i], x[i], acc_post[j][2 * q + i]);
+                                acc_post[j][2 * k + i] = f2_fma(d[i], x[i], acc_post[j][2 * k + i]);
                             }
                             f[i] = f2_fma(my, x[i], f2_mul(f[i], d[i]));
                         }
@@ -579,11 +594,11 @@ __global__ void __launch_bounds__(kNormGradThreads) block_norm_grad_kernel(Block
     float* part = a.partials + (long long)blockIdx.x * 2 * a.H;
     auto put_sums = [&](float* dst, const f2* s) {
 #pragma unroll
-        for (int i = 0; i < N / 2; i += 2) {
+        for (int k = 0; k < kQ; ++k) {
             float4 x;
-            f2_split(s[i], x.x, x.y);
-            f2_split(s[i + 1], x.z, x.w);
-            *reinterpret_cast<float4*>(dst + 2 * i) = x;
+            f2_split(s[2 * k], x.x, x.y);
+            f2_split(s[2 * k + 1], x.z, x.w);
+            *reinterpret_cast<float4*>(dst + 4 * (k ^ swap)) = x;
         }
     };
 #pragma unroll
