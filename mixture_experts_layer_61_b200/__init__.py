@@ -9,6 +9,7 @@ device other than sm_100, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 
@@ -168,9 +169,14 @@ def _need_cuda(*ts):
             raise ValueError("tensors must be contiguous CUDA tensors")
 
 
+@functools.lru_cache(maxsize=None)
+def _device(index):
+    return torch.device("cuda", index)
+
+
 def _dev():
     # before CUDA is initialised no tensor can be on a device: any index refuses them
-    return torch.device("cuda", torch.cuda.current_device() if torch.cuda.is_initialized() else 0)
+    return _device(torch.cuda.current_device() if torch.cuda.is_initialized() else 0)
 
 
 def _arg(name, t, shape, dtype, dev=None):
