@@ -165,11 +165,12 @@ int launch_variant(const GemmLaunch& L, const GemmCtl& ctl, int num_sms, cudaStr
     p.status = ctl.status;
     p.wait_limit_ns = wait_limit_ns();
     p.withhold_first_load = take_withhold_flag();
-    // fewest k-iterations of a slice; training: 16 where tiles hold many tokens,
-    // whose partial sums take longer than that to add up (8 experts of 1024 x
-    // 1024, 512 tokens, down gradient: 28 us whole, 39 us in slices of 4; with 8
-    // tokens in all, gate/up gradient: 25 us whole, 18 us in slices)
-    p.sk_min_units = kTrain && L.x_rows > 64LL * L.n_groups ? 16 / C::kChunks : 4 / C::kChunks;
+    // fewest k-iterations of a slice; training: 16, as adding up a slice's partial
+    // sums takes longer than fewer (8 experts of 512 x 512, 192 tokens, gate/up
+    // gradient: 13.5 us, in slices of 4 26.3 us; 64 of 1024 x 512, 64 tokens:
+    // 14.4 us, 20.7 us; only a single token gains from slices of 4: 8 of 2048 x
+    // 1024, gate/up with pre-activations: 15.8 us, 14.4 us)
+    p.sk_min_units = (kTrain ? 16 : 4) / C::kChunks;
     p.max_split = L.max_split > 0 ? L.max_split : 4;
     p.split_tail = split_tail_mode();
     int grid = grid_blocks;
