@@ -959,9 +959,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             // contributor i: a block (contiguous) or a slice (aligned), in k order
                             int c, slot;
                             if (aligned) {
+                                // at most two slices a block (aligned_slices): no division
                                 const long long q = it.sk_tile + (long long)i * sch.sk_tiles;
-                                c = (int)(q % sch.G);
-                                slot = (int)(q / sch.G);
+                                slot = q >= sch.G;
+                                c = (int)(q - (slot ? sch.G : 0));
                             } else {
                                 c = i;
                                 const long long bc = sch.beg(c);
