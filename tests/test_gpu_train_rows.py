@@ -365,3 +365,10 @@ def test_two_norm_gradients_at_once():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(torch.equal(a[k], b[k]) for k in b)
+
+
+@pytest.mark.parametrize("dt,H", [("bf16", 16384), ("bf16", 12296), ("fp32", 8192), ("fp32", 4100)])
+@pytest.mark.parametrize("post,gate_mode,nxt", [(True, 2, True), (True, 1, True), (False, 0, True), (True, 2, False)])
+def test_norm_gradient_of_long_rows_several_to_a_block(dt, H, post, gate_mode, nxt):
+    """Rows that fill a block's shared memory (one to three at once), more rows than blocks."""
+    test_block_norm_grad(331, H, post, gate_mode, nxt, dt)
