@@ -193,6 +193,9 @@ int launch_route_small(int T, int H, int E, int K, int score_fn, int renorm, int
                        const int32_t* k_per_token, float* part, float* logits, int32_t* ids, float* w,
                        int32_t* counts, int32_t* offsets, int32_t* sorted_ids, int32_t* block_expert, int32_t* pos,
                        int32_t* scalars, int32_t* stats_copy, int* done_ctr, cudaStream_t stream);
+// 16-byte vectors of n activations, n a multiple of one's: by division, as the
+// bytes of the longest rows pass 32 bits.
+inline int vectors_of(int n, int dtype) { return n / (dtype == 0 ? 8 : 4); }
 int launch_permute(int H, int K, int dtype, long long P_max, const void* x, const int32_t* sorted_ids,
                    const int32_t* scalars, void* x_perm, cudaStream_t stream);
 // The exact two-term E4M3 split of bf16 rows [rows, H] (gathered by

@@ -1288,7 +1288,7 @@ int launch_combine(int T, int H, int K, int dtype, const void* y_perm, const int
 int launch_permute_grad(int T, int H, int K, int dtype, const void* dx_perm, const int32_t* pos, const void* dx_add,
                         void* dx, cudaStream_t stream) {
     if (T == 0) return 0;
-    const int row_vec = H * (dtype == 0 ? 2 : 4) / 16;
+    const int row_vec = vectors_of(H, dtype);
     const int threads = 256;
     long long blocks = ((long long)T * row_vec + threads - 1) / threads;
     if (blocks > 0x7fffffffLL) blocks = 0x7fffffffLL;
