@@ -1087,7 +1087,7 @@ int moe_layer_forward_partial_down(const moe_config_t* cfg, const void* w2, int 
     if (n_chunks < 1 || chunk < 0 || chunk >= n_chunks || cfg->H % n_chunks) return MOE_ERR_ARG;
     const int eb = elt_bytes(cfg->dtype);
     const int Hc = cfg->H / n_chunks, c0 = chunk * Hc;
-    if ((Hc * eb) % 16 || Hc % 4) return MOE_ERR_ARG;  // 16-byte vectors in, float4 out
+    if (Hc % (16 / eb) || Hc % 4) return MOE_ERR_ARG;  // 16-byte vectors in, float4 out
     if (routed_max_n(cfg) <= 128) return MOE_ERR_ARG;   // the two-launch expert FFN only
     if (cfg->T == 0) return MOE_OK;
     if (!w2 || !part || !workspace || !aligned16(w2) || !aligned16(part) || !aligned16(workspace)) return MOE_ERR_ARG;

@@ -1068,8 +1068,7 @@ int launch_permute(int H, int K, int dtype, long long P_max, const void* x, cons
     DeviceInfo d;
     int rc = current_device(&d);
     if (rc != 0) return rc;
-    const int elt = dtype == 0 ? 2 : 4;
-    const int row_vec = H * elt / 16;
+    const int row_vec = vectors_of(H, dtype);
     long long rows_per_block = 4;
     long long blocks = (P_max + rows_per_block - 1) / rows_per_block;
     const long long cap = (long long)d.num_sms * 8;
@@ -1249,11 +1248,10 @@ int launch_combine(int T, int H, int K, int dtype, const void* y_perm, const int
     DeviceInfo d;
     int rc = current_device(&d);
     if (rc != 0) return rc;
-    const int elt = dtype == 0 ? 2 : 4;
-    const int row_vec = H * elt / 16;
+    const int row_vec = vectors_of(H, dtype), vec = dtype == 0 ? 8 : 4;
     if (ncols < 0) col0 = 0, ncols = H;
-    if ((col0 * elt) % 16 || (ncols * elt) % 16 || col0 < 0 || col0 + ncols > H) return -1;
-    const int c0 = col0 * elt / 16, nc = ncols * elt / 16;
+    if (col0 % vec || ncols % vec || col0 < 0 || ncols > H - col0) return -1;
+    const int c0 = vectors_of(col0, dtype), nc = vectors_of(ncols, dtype);
     const int threads = 256;
     // one thread per output vector (a grid of up to 2^31 - 1 blocks covers
     // every layer this library accepts; beyond that the threads stride)

@@ -29,6 +29,19 @@ def same(out, ref):
 
 
 @pytest.mark.parametrize("H,dtype", CASES)
+def test_permute(H, dtype):
+    cfg, al, x = one_token(H, dtype)
+    assert same(moe.permute(cfg, x, al["sorted_ids"], al["scalars"]), x)
+
+
+@pytest.mark.parametrize("H,dtype", CASES)
+def test_combine(H, dtype):
+    cfg, al, y = one_token(H, dtype)
+    w = torch.full((1, 1), 0.5, device="cuda")
+    assert same(moe.combine(cfg, y, al["pos"], w), y.mul_(0.5))  # halves are exact
+
+
+@pytest.mark.parametrize("H,dtype", CASES)
 def test_permute_grad(H, dtype):
     cfg, al, d = one_token(H, dtype)
     extra = d.flip(1)
