@@ -821,20 +821,23 @@ def block_norm_grad(nc, ws, h=None, dh=None, dn=None, y=None, w_post=None, gate=
     return dict(dw_next=dw_next, dresidual=dresidual, dgate=dgate, dw_post=dw_post, dy=dy)
 
 
-def _product(cfg, ws, offsets, rows, weights=None):
-    """Checks of a training product: (device, (given or new) row buffers)."""
+def _product(cfg, ws, offsets, rows, outs=(), weights=None):
+    """Checks of a training product: (device, the row buffers of `outs`, given or new)."""
     dt, dev, R = _act_dtype(cfg), _dev(), max(padded_rows_max(cfg), 1)
     _arg("offsets", offsets, (cfg.E + 1,), torch.int32, dev)
     _arg("ws", ws, (ws.numel(),), torch.uint8, dev)
     if weights is not None:
         _arg(weights[0], weights[1], weights[2], dt, dev)
-    out, like = [], None
     for name, t, width in rows:
         if t is None:
-            t = like.new_empty((R, width))
+            raise ValueError(f"{name} must be given")
+        _arg(name, t, (R, width), dt, dev)
+    out = []
+    for name, t, width in outs:
+        if t is None:
+            t = rows[0][1].new_empty((R, width))
         else:
             _arg(name, t, (R, width), dt, dev)
-        like = t
         out.append(t)
     return dev, out
 
@@ -842,8 +845,8 @@ def _product(cfg, ws, offsets, rows, weights=None):
 def grouped_gate_up_train(cfg, x_perm, w13, offsets, ws, h13=None, act=None):
     """(h13, act): gate/up with the pre-activations [P_max, 2I] kept."""
     I = cfg.I
-    dev, (x_perm, h13, act) = _product(cfg, ws, offsets, (("x_perm", x_perm, cfg.H), ("h13", h13, 2 * I),
-                                                          ("act", act, I)), ("w13", w13, (cfg.E, 2 * I, cfg.H)))
+    dev, (h13, act) = _product(cfg, ws, offsets, (("x_perm", x_perm, cfg.H),), (("h13", h13, 2 * I), ("act", act, I)),
+                               ("w13", w13, (cfg.E, 2 * I, cfg.H)))
     _check(lib().moe_grouped_gate_up_train(ctypes.byref(cfg), _a(x_perm), _a(w13), _a(offsets), _a(h13), _a(act),
                                            _a(ws), ws.numel(), _raw_stream(dev)), "moe_grouped_gate_up_train")
     return h13, act
@@ -852,8 +855,8 @@ def grouped_gate_up_train(cfg, x_perm, w13, offsets, ws, h13=None, act=None):
 def grouped_down_grad(cfg, dy_perm, w2, h13, offsets, ws, dh13=None):
     """dh13: the gradient through the down projection and SwiGLU (may be h13)."""
     I = cfg.I
-    dev, (dy_perm, h13, dh13) = _product(cfg, ws, offsets, (("dy_perm", dy_perm, cfg.H), ("h13", h13, 2 * I),
-                                                            ("dh13", dh13, 2 * I)), ("w2", w2, (cfg.E, cfg.H, I)))
+    dev, (dh13,) = _product(cfg, ws, offsets, (("dy_perm", dy_perm, cfg.H), ("h13", h13, 2 * I)),
+                            (("dh13", dh13, 2 * I),), ("w2", w2, (cfg.E, cfg.H, I)))
     _check(lib().moe_grouped_down_grad(ctypes.byref(cfg), _a(dy_perm), _a(w2), _a(h13), _a(offsets), _a(dh13), _a(ws),
                                        ws.numel(), _raw_stream(dev)), "moe_grouped_down_grad")
     return dh13
@@ -862,8 +865,8 @@ def grouped_down_grad(cfg, dy_perm, w2, h13, offsets, ws, dh13=None):
 def grouped_gate_up_grad(cfg, dh13, w13, offsets, ws, dx_perm=None):
     """dx_perm: the gradient through the gate/up projections."""
     I = cfg.I
-    dev, (dh13, dx_perm) = _product(cfg, ws, offsets, (("dh13", dh13, 2 * I), ("dx_perm", dx_perm, cfg.H)),
-                                    ("w13", w13, (cfg.E, 2 * I, cfg.H)))
+    dev, (dx_perm,) = _product(cfg, ws, offsets, (("dh13", dh13, 2 * I),), (("dx_perm", dx_perm, cfg.H),),
+                               ("w13", w13, (cfg.E, 2 * I, cfg.H)))
     _check(lib().moe_grouped_gate_up_grad(ctypes.byref(cfg), _a(dh13), _a(w13), _a(offsets), _a(dx_perm), _a(ws),
                                           ws.numel(), _raw_stream(dev)), "moe_grouped_gate_up_grad")
     return dx_perm
