@@ -579,7 +579,8 @@ __global__ void __launch_bounds__(kNormGradThreads) block_norm_grad_kernel(Block
                             } else {
                                 acc_post[j][2 * k + i] = f2_fma(d[i], x[i], acc_post[j][2 * k + i]);
                             }
-                            f[i] = f2_fma(my, x[i], f2_mul(f[i], d[i]));
+                            f[i] = f2_mul(f[i], d[i]);
+                            if (post) f[i] = f2_fma(my, x[i], f[i]);  // else not of y: it may be infinite or NaN
                         }
                         if (kGate == 2) put_quad(static_cast<int4*>(a.dgate) + o, q, dg, tag);
                         put_quad(static_cast<int4*>(a.dy) + o, q, f, tag);
