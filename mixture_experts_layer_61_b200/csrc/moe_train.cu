@@ -660,11 +660,12 @@ __global__ void __launch_bounds__(kWgradGroups * kWgradCols / 4) norm_wgrad_kern
         return;
     }
     const float f[4] = {s.x, s.y, s.z, s.w};
-    const T* g = static_cast<const T*>(a.gate);
-    const T* w = static_cast<const T*>(a.w_post);
+    // without tokens the sums are zero whatever the weights are
+    const T* g = n_parts && a.gate_mode == 1 ? static_cast<const T*>(a.gate) : nullptr;
+    const T* w = n_parts ? static_cast<const T*>(a.w_post) : nullptr;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        if (a.dw_post) a.dw_post[c + i] = a.gate_mode == 1 ? Elt<T>::to_f(g[c + i]) * f[i] : f[i];
+        if (a.dw_post) a.dw_post[c + i] = g ? Elt<T>::to_f(g[c + i]) * f[i] : f[i];
         if (a.gate_mode == 1 && a.dgate)
             static_cast<float*>(a.dgate)[c + i] = w ? Elt<T>::to_f(w[c + i]) * f[i] : f[i];
     }

@@ -27,3 +27,16 @@ def test_without_a_norm_after_the_block_dy_does_not_depend_on_y(H, gate_mode, dt
     # one fp32 product and one rounding (none without a gate)
     R.close(r["dy"], ref, (R.HALF[dtype] + 2.0 ** -23) * ref.abs(), "dy")
     assert torch.equal(r["dresidual"], (0.5 * dh.float()).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_zero_tokens_write_zeros_beside_infinite_weights(dtype):
+    H = 264
+    nc = moe.norm_config(0, H, gate_mode=moe.GATE_CHANNEL, dtype=dtype)
+    w = torch.ones(H, dtype=dtype, device="cuda")
+    w[0], w[1], w[2] = float("inf"), float("-inf"), float("nan")
+    e = torch.empty((0, H), dtype=dtype, device="cuda")
+    ws = moe.alloc_workspace(moe.block_norm_grad_workspace_size(nc))
+    r = moe.block_norm_grad(nc, ws, h=e, dh=e, dn=e, y=e, w_post=w, gate=w, w_next=w)
+    for k in ("dw_next", "dw_post", "dgate"):
+        assert not r[k].any(), k
