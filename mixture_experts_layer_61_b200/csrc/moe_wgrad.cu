@@ -62,7 +62,6 @@ struct WgradParams {
 struct WgItem {
     int g, m0, n0, tiles;
     int row0, steps;   // steps: 16-row MMA steps
-    bool resident;     // the d panel stays for all tiles
 };
 
 // The units of one CTA pair, the same sequence for each of its roles.  Experts
@@ -127,7 +126,6 @@ struct WgSched {
             it.m0 = (int)mt * 256;
             it.n0 = first * 256;
         }
-        it.resident = !stream;
         it.g = order[e];
         it.row0 = seg[it.g];
         const int rows = seg[it.g + 1] - it.row0;
