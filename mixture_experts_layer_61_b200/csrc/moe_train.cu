@@ -4,7 +4,8 @@
 // block's gate and residual scale, fused with the combine) with their
 // gradient.  All are bound by device memory at training sizes and by latency
 // at decode sizes: each reads its rows once, keeps its sums in fp32 and rounds
-// each output once.
+// each output once.  Times in this file are of calls back to back, inputs larger
+// than L2, unless said otherwise.
 #include <atomic>
 #include <climits>
 #include <type_traits>
@@ -126,7 +127,8 @@ bool row_kernels_fit(int H, int dtype) { return H <= 32 * 1024 / (dtype == 0 ? 2
 // the last store, so every output is rounded once; the K rows' vectors are all
 // requested before the first is used.  2048 tokens of 3584 bf16, K = 8, shared
 // output, both norms: 41 us, 191 MB (0.72 of the copy bandwidth); one token
-// 2.9 us.
+// 2.7 us in a graph.  Without the combine, 4096 of 7168, gate and both norms:
+// 63 us, 235 MB (0.58).
 template <typename T, int kV, int kMaxK>
 __global__ void __launch_bounds__(kNormThreads, kV <= 2 && kMaxK <= 8 ? 3 : 2) block_norm_kernel(BlockNormArgs a) {
     constexpr int N = Vec16<T>::N;
@@ -761,7 +763,8 @@ int launch_block_norm_grad(const BlockNormGradArgs& a, cudaStream_t stream) {
 // One block per token: dout's row is read once into registers and meets the K
 // rows it scales and is dotted with.  The blocks past the tokens zero the
 // padding rows (the weight gradients multiply them).  4096 tokens of 7168
-// bf16, K = 8: 196 us, 1.0 GB (0.79 of the copy bandwidth).
+// bf16, K = 8: 177 us (a single call 184 us), 1.0 GB (0.87 of the copy
+// bandwidth).
 template <typename T, int kV, int kMaxK>
 __global__ void __launch_bounds__(kNormThreads, 2) combine_grad_kernel(CombineGradArgs a) {
     constexpr int N = Vec16<T>::N;
@@ -894,7 +897,8 @@ int launch_combine_grad(const CombineGradArgs& args, cudaStream_t stream) {
 // 1 - s is taken as the sigmoid of -l, so it keeps its digits near s = 1.
 // The row is zeroed (or given the full softmax's share), then the selected
 // entries are written; a repeated expert's shares are added first.  Bound by
-// latency: 2048 tokens x 256 experts, K = 8: 2.8 us, 2.3 MB.
+// latency: 2048 tokens x 256 experts, K = 8, in a graph: 2.6 us, 2.3 MB on the
+// selected logits; the full softmax, which passes over the row three times, 4.9 us.
 __global__ void __launch_bounds__(256) route_grad_kernel(int T, int E, int K, int score_fn, int renorm,
                                                          const float* __restrict__ logits,
                                                          const int32_t* __restrict__ ids,

@@ -18,9 +18,11 @@
 // shared memory and stores it by TMA, which clips at the weight's own edges.
 //
 // Qwen2-MoE-shaped gate/up weights (64 x 5120 x 3584, 16384 rows, experts very
-// uneven): 725 us, 2.35 GB written and 0.6 TFLOP; with even experts of at most
-// 256 rows (12800 rows) 590 us.  The first version, d and x streamed for
-// every tile and one 4 KB staging block per warp, took 968 us.
+// uneven): 729 us for a single call (838 us back to back, at the clock the power
+// cap leaves), 2.35 GB written and 0.6 TFLOP; with even experts of at most 256
+// rows (12800 rows) 590 us.  The first version, d and x streamed for every tile
+// and one 4 KB staging block per warp, took 968 us.  Times in this file are of
+// single calls.
 //
 // Segments are whole multiples of 16 rows (the MMA's K), their padding rows
 // zero in both operands; a stage reads up to 63 rows past its segment, but
